@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libdg.so")
 DG_OK, DG_ERR_INVALID_ARG, DG_ERR_UNSUPPORTED, DG_ERR_CAPACITY, DG_ERR_CUDA, \
     DG_ERR_NUMERIC, DG_ERR_TIMEOUT, DG_ERR_WORKSPACE = range(8)
 DG_F32, DG_BF16, DG_E4M3, DG_NVFP4 = 0, 1, 2, 3
+DG_ROPE_HALF, DG_ROPE_INTERLEAVED = 0, 1
+DG_ROPE_UNSCALED, DG_ROPE_LINEAR, DG_ROPE_BY_PARTS = 0, 1, 2
 STATUS_NAMES = {0: "DG_OK", 1: "DG_ERR_INVALID_ARG", 2: "DG_ERR_UNSUPPORTED", 3: "DG_ERR_CAPACITY",
                 4: "DG_ERR_CUDA", 5: "DG_ERR_NUMERIC", 6: "DG_ERR_TIMEOUT", 7: "DG_ERR_WORKSPACE"}
 
@@ -66,10 +68,31 @@ def make_sampler(tau_start=0.0, tau_end=None, seed=0, revise=False) -> DgSampler
                      int(seed) & 0xFFFFFFFFFFFFFFFF, 1 if revise else 0)
 
 
+class DgRope(ctypes.Structure):
+    """dg_rope: rotated part of a head, pair layout and frequency scaling."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("orig_len", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("mscale", ctypes.c_double)]
+
+
+def make_rope(rot_dim, layout=DG_ROPE_HALF, scaling=DG_ROPE_UNSCALED, factor=1.0, orig_len=0.0,
+              beta_slow=1.0, beta_fast=32.0, mscale=1.0) -> DgRope:
+    return DgRope(int(rot_dim), int(layout), int(scaling), float(factor), float(orig_len),
+                  float(beta_slow), float(beta_fast), float(mscale))
+
+
+class DgPagedKv(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 _VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _PCFG, _PMODEL, _PLW = ctypes.POINTER(DgConfig), ctypes.POINTER(DgModel), ctypes.POINTER(DgLayerWeights)
 _PSMP = ctypes.POINTER(DgSampler)
+_PROPE, _PKV = ctypes.POINTER(DgRope), ctypes.POINTER(DgPagedKv)
 
 _SIGS = {
     "dg_workspace_size": (_SZ, [_PCFG, _I32, _I32, _I32]),
@@ -103,6 +126,14 @@ _SIGS = {
                                       _VP, _VP, _SZ, _VP, _VP]),
     "dg_debug_wait_probe": (_I32, [ctypes.c_longlong, _I32, _VP, _VP]),
     "dg_noise_canvas": (_I32, [_I32, _I32, _I32, ctypes.c_uint64, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "dg_qk_norm_rope": (_I32, [_PCFG, _I32, _I32, _VP, ctypes.c_longlong, _VP, _VP, _VP, _PROPE, _VP,
+                               _VP, _VP, _VP, _VP]),
+    "dg_paged_append": (_I32, [_PCFG, _I32, _I32, _VP, _VP, _VP, ctypes.c_longlong, _VP, _VP, _PROPE,
+                               _PKV, _VP, _VP, _VP]),
+    "dg_paged_workspace_size": (_SZ, [_PCFG, _I32, _I32, _I32]),
+    "dg_paged_attn": (_I32, [_PCFG, _I32, _I32, _VP, _VP, _VP, _PKV, _I32, _VP, _VP, _SZ, _VP, _VP]),
+    "dg_prefix_attn": (_I32, [_PCFG, _I32, _I32, _VP, _VP, _I32, _VP, _PKV, _I32, _VP, _VP, _SZ, _VP,
+                              _VP]),
     "dg_ar_step": (_I32, [_PCFG, _PMODEL, _I32, _VP, _I32, _VP, _VP, _VP, _I32, _PSMP, _VP, _VP,
                           _VP, _VP, _VP, _SZ, _VP, _VP]),
 }
@@ -354,6 +385,131 @@ def dg_ar_step(cfg, model: Model, batch, tokens, n_tokens, k_cache, v_cache, cac
                             _p(entropy), _p(logits_dbg), _p(forced_topk), w, wb, _p(dev_status),
                             _stream(stream)),
            "dg_ar_step")
+
+
+# ----------------------------------------------------------------------------- paged cache
+
+class PagedKV:
+    """Host-side dg_paged_kv over one layer's pages: k_pages, v_pages [n_pages][Hkv][page][hd] and
+    the int32 page table [n_seqs][max_pages] (keeps the tensors alive)."""
+
+    def __init__(self, k_pages, v_pages, page_table):
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+            raise ValueError("k_pages and v_pages are alike, [n_pages][Hkv][page][hd]")
+        if page_table.dim() != 2 or page_table.dtype != torch.int32:
+            raise ValueError("the page table is int32 [n_seqs][max_pages]")
+        self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
+        self.struct = DgPagedKv(_p(k_pages), _p(v_pages), _p(page_table), k_pages.shape[0],
+                                k_pages.shape[2], page_table.shape[1])
+        self.ref = ctypes.byref(self.struct)
+
+
+_ACT = {DG_F32: torch.float32, DG_BF16: torch.bfloat16}
+
+
+def _rows(t, name, dtype, *shape):
+    """Pointer of a contiguous device tensor of this type that holds exactly `shape`."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: {dtype} {shape} wanted, {t.dtype} {tuple(t.shape)} given")
+    return _p(t)
+
+
+def _qkv_rows(cfg, qkv, rows):
+    """Pointer and row stride of projected rows [rows][(Hq + 2 Hkv) hd]; the rows may lie apart."""
+    width = (cfg.n_q_heads + 2 * cfg.n_kv_heads) * cfg.head_dim
+    if qkv.dtype != _ACT[cfg.act_dtype] or qkv.shape != (rows, width):
+        raise ValueError(f"qkv: {_ACT[cfg.act_dtype]} {(rows, width)} wanted, "
+                         f"{qkv.dtype} {tuple(qkv.shape)} given")
+    if not qkv.is_cuda or qkv.stride(1) != 1:
+        raise ValueError("qkv: device rows of contiguous elements wanted")
+    return qkv.data_ptr(), (qkv.stride(0) if rows > 1 else width)
+
+
+def _gain(cfg, g, name):
+    return None if g is None else _rows(g, name, torch.float32, cfg.head_dim)
+
+
+def _pages(cfg, kv: PagedKV, n_seqs):
+    k = kv.k_pages
+    if k.dtype != _ACT[cfg.act_dtype] or k.shape[1] != cfg.n_kv_heads or k.shape[3] != cfg.head_dim:
+        raise ValueError("the pages do not fit the config")
+    if kv.page_table.shape[0] < n_seqs:
+        raise ValueError("the page table has fewer rows than there are sequences")
+    return kv.ref
+
+
+def _index(t, name, n):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < n:
+        raise ValueError(f"{name}: int32 of at least {n} wanted")
+    return _p(t)
+
+
+def _launch(fn, what, device, stream, *args):
+    """fn(*args, stream) on the tensors' device, which need not be the current one."""
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(stream))
+    _check(rc, what)
+
+
+def dg_qk_norm_rope(cfg, batch, n_tokens, qkv, cache_len, q_gain, k_gain, rope: Optional[DgRope], q,
+                    k_new, v_new, dev_status=None, stream=None):
+    """Per-head norms, rotation and head split of projected rows (ready for dg_canvas_attn)."""
+    ptr, ld = _qkv_rows(cfg, qkv, batch * n_tokens)
+    act, hd, hkv = _ACT[cfg.act_dtype], cfg.head_dim, cfg.n_kv_heads
+    _launch(lib().dg_qk_norm_rope, "dg_qk_norm_rope", qkv.device, stream, ctypes.byref(cfg), batch,
+            n_tokens, ptr, ld, _index(cache_len, "cache_len", batch), _gain(cfg, q_gain, "q_gain"),
+            _gain(cfg, k_gain, "k_gain"), None if rope is None else ctypes.byref(rope),
+            _rows(q, "q", act, batch, n_tokens, cfg.n_q_heads, hd),
+            _rows(k_new, "k_new", act, batch, hkv, n_tokens, hd),
+            _rows(v_new, "v_new", act, batch, hkv, n_tokens, hd), _p(dev_status))
+
+
+def dg_paged_append(cfg, n_seqs, n_tokens, seq_off, kv_len, qkv, q_gain, k_gain,
+                    rope: Optional[DgRope], kv: PagedKV, q, dev_status=None, stream=None):
+    """Per-head norms and rotation of packed rows; q packed, K and V into their pages."""
+    ptr, ld = _qkv_rows(cfg, qkv, n_tokens)
+    _launch(lib().dg_paged_append, "dg_paged_append", qkv.device, stream, ctypes.byref(cfg), n_seqs,
+            n_tokens, _index(seq_off, "seq_off", n_seqs + 1), _index(kv_len, "kv_len", n_seqs), ptr,
+            ld, _gain(cfg, q_gain, "q_gain"), _gain(cfg, k_gain, "k_gain"),
+            None if rope is None else ctypes.byref(rope), _pages(cfg, kv, n_seqs),
+            None if q is None else _rows(q, "q", _ACT[cfg.act_dtype], n_tokens, cfg.n_q_heads,
+                                         cfg.head_dim), _p(dev_status))
+
+
+def dg_paged_workspace_size(cfg, n_seqs, n_tokens, shared_len=0) -> int:
+    return lib().dg_paged_workspace_size(ctypes.byref(cfg), n_seqs, n_tokens, shared_len)
+
+
+def alloc_paged_workspace(cfg, n_seqs, n_tokens, shared_len=0, device="cuda"):
+    n = dg_paged_workspace_size(cfg, n_seqs, n_tokens, shared_len)
+    if n == 0:
+        raise DgError(DG_ERR_INVALID_ARG, "dg_paged_workspace_size")
+    return torch.empty(n + 256, dtype=torch.uint8, device=device)
+
+
+def dg_paged_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, q, kv: PagedKV, causal, out, ws,
+                  dev_status=None, stream=None):
+    """Attention of packed sequences over their pages (the new K and V already appended)."""
+    w, wb = _ws(ws)
+    act, hq, hd = _ACT[cfg.act_dtype], cfg.n_q_heads, cfg.head_dim
+    _launch(lib().dg_paged_attn, "dg_paged_attn", q.device, stream, ctypes.byref(cfg), n_seqs,
+            n_tokens, _index(seq_off, "seq_off", n_seqs + 1), _index(kv_len, "kv_len", n_seqs),
+            _rows(q, "q", act, n_tokens, hq, hd), _pages(cfg, kv, n_seqs), 1 if causal else 0,
+            _rows(out, "out", act, n_tokens, hq, hd), w, wb, _p(dev_status))
+
+
+def dg_prefix_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, shared_len, q, kv: PagedKV, causal, out,
+                   ws, dev_status=None, stream=None):
+    """dg_paged_attn where the first shared_len keys are common to all sequences, read once."""
+    w, wb = _ws(ws)
+    act, hq, hd = _ACT[cfg.act_dtype], cfg.n_q_heads, cfg.head_dim
+    _launch(lib().dg_prefix_attn, "dg_prefix_attn", q.device, stream, ctypes.byref(cfg), n_seqs,
+            n_tokens, _index(seq_off, "seq_off", n_seqs + 1), _index(kv_len, "kv_len", n_seqs),
+            shared_len, _rows(q, "q", act, n_tokens, hq, hd), _pages(cfg, kv, n_seqs),
+            1 if causal else 0, _rows(out, "out", act, n_tokens, hq, hd), w, wb, _p(dev_status))
 
 
 def dg_debug_wait_probe(limit_cycles, arrive, dev_status, stream=None):

@@ -91,6 +91,47 @@ int launch_attention_tc(int batch, int n, int Hq, int Hkv, int hd, const void *q
                         const void *k_new, const void *v_new, int causal, const int32_t *done,
                         void *out, void *ws, int32_t *st, cudaStream_t s);
 
+// ---- rows of a QKV projection: norms, rotation, split (k_qkv_rows.cu) ---------------------------
+struct RopeSpec {
+  double theta;
+  int rot, interleaved, scaling;   // rot: rotated elements of a head, a multiple of 16
+  double factor, orig_len, beta_slow, beta_fast, mscale;
+};
+struct QkvCall {
+  int act, hd, Hq, Hkv;
+  double eps;
+  const void *qkv;                 // [n_tokens] rows, ld elements apart
+  long long ld;
+  int n_tokens, n_seqs, n;         // n > 0: n rows per sequence, K/V to k, v [n_seqs][Hkv][n][hd]
+  const int32_t *seq_off, *len;    // n == 0: packed by seq_off, K/V to the pages
+  const float *q_gain, *k_gain;    // null: no norm
+  RopeSpec rope;
+  void *q, *k, *v;                 // q may be null
+  void *k_pages, *v_pages;
+  const int32_t *page_table;
+  int n_pages, page_size, max_pages;
+  int32_t *status;
+};
+int launch_qkv_rows(const QkvCall &c, cudaStream_t s);
+
+// ---- attention over a paged cache (k_paged_attn.cu) ---------------------------------------------
+struct PagedCall {
+  int act, hd, Hq, Hkv;
+  int n_seqs, n_tokens, causal;
+  int shared_len;                  // 0: no shared prefix
+  const int32_t *seq_off, *kv_len;
+  const void *q;
+  void *out;
+  const void *k_pages, *v_pages;
+  const int32_t *page_table;
+  int n_pages, page_size, max_pages;
+  int32_t *status;
+};
+bool paged_attn_supported(int act, int Hq, int Hkv, int hd);
+// Uses act, hd, head counts, n_tokens and shared_len of the call.
+size_t paged_attn_ws_bytes(const PagedCall &c);
+int launch_paged_attn(const PagedCall &c, void *ws, cudaStream_t s);
+
 // ---- MoE (k_moe.cu) ---------------------------------------------------------------------------
 // n_shared: shared experts E .. E + n_shared - 1 appended to every live token's slots (gate 1);
 // the outputs are then [T][k + n_shared].

@@ -1,0 +1,429 @@
+// Attention of packed sequences over a paged K/V cache: the CUDA-core kernel (fp32 activations,
+// and bf16 with heads of 32) and the kernels that join partial results.
+//
+// "DiffusionGemma Technical Report", Figure 4: a prompt is encoded causally into a K/V cache and a
+// canvas attends to it bidirectionally; the cache here lies in pages, and sequences of different
+// lengths share a launch (paged_plan.cuh splits the work).
+//   o = softmax(q K^T / sqrt(hd)) V,  with t = q.k / sqrt(hd) * log2(e):
+//   m = max t, l = sum 2^(t - m), O = sum 2^(t - m) v, out = O / l
+// and partial results of disjoint key sets join as m = max m_i, l = sum l_i 2^(m_i - m),
+// O = sum O_i 2^(m_i - m).  Scores, statistics and O are fp32; the output is rounded once.
+#include "dg_common.cuh"
+#include "dg_kernels.h"
+#include "paged_attn.cuh"
+#include "tc_host.h"
+
+namespace dg {
+
+namespace {
+
+constexpr int S_ROWS = 64, S_KT = 64, S_THR = 256;
+
+template <int HD>
+constexpr size_t simt_smem() {
+  return (size_t)(2 * S_ROWS * (HD + 4) + S_ROWS * (S_KT + 4)) * sizeof(float);
+}
+
+// Four consecutive elements as fp32.
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const bf16 *p) {
+  const uint2 v = *reinterpret_cast<const uint2 *>(p);
+  const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162 *>(&v.x);
+  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162 *>(&v.y);
+  return make_float4(__low2float(a), __high2float(a), __low2float(b), __high2float(b));
+}
+
+// One CTA walks its range of (item, key tile) units: 64 query rows (token-major, the heads of a
+// group within a token) against tiles of 64 keys.  Thread (tx, ty) of 16 x 16 holds rows 4 ty ..
+// 4 ty + 3: scores of keys tx + 16 j, then output columns.  K and V take turns in one tile buffer,
+// so that two CTAs fit an SM and one computes while the other loads.
+template <typename T, int HD>
+__global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(PagedShape p, PagedIO io) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int LD = HD + 4, LP = S_KT + 4;   // padded rows: conflict-free float4 reads
+  constexpr int DPT = HD / 16, VEC = DPT < 4 ? DPT : 4, NV = DPT / VEC;
+  extern __shared__ __align__(16) float simt_smem_raw[];
+  float *Qs = simt_smem_raw, *KVs = Qs + S_ROWS * LD, *Ps = KVs + S_KT * LD;
+  __shared__ PagedStart start_s;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  if (tid < 32) {
+    int err;
+    const PagedStart st = paged_locate(p, blockIdx.x, gridDim.x, &err);
+    if (tid == 0) {
+      start_s = st;
+      if (blockIdx.x == 0) paged_report(io, err);
+      paged_write_head(p, io, st, blockIdx.x);
+    }
+  }
+  __syncthreads();
+  const PagedStart st = start_s;
+  const int rep = io.rep;
+  const float sl2 = 1.4426950408889634f * rsqrtf((float)HD);
+  PagedWalk w;
+  for (w.begin(p, st); w.more(); w.next(p)) {
+    const PagedSeg s = w.s;
+    const int k0 = w.k0(), k1 = w.k1();
+    const int i0 = w.item * p.qt, toks = paged_item_tokens(p, s, w.item), rows = toks * rep;
+    const int item_keys = paged_item_keys(p, s, w.item);
+    __syncthreads();  // the last piece's readers of Qs and KVs are done
+    for (int e = tid; e < S_ROWS * (HD / 4); e += S_THR) {
+      const int r = e / (HD / 4), c = e % (HD / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows)
+        v = load4((const T *)io.q +
+                  ((size_t)(s.tok0 + i0 + r / rep) * io.Hq + w.head * rep + r % rep) * HD + c);
+      *reinterpret_cast<float4 *>(&Qs[r * LD + c]) = v;
+    }
+    float o[4][DPT], m[4], l[4];
+    int lim[4];  // keys this row sees
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      lim[i] = s.causal ? s.keys - s.n + i0 + min(r / rep, toks - 1) + 1 : s.keys;
+#pragma unroll
+      for (int d = 0; d < DPT; ++d) o[i][d] = 0.f;
+    }
+    for (int t = k0; t < k1; ++t) {
+      const int j0 = t * S_KT;
+      auto load_tile = [&](const void *pages) {
+        for (int e = tid; e < S_KT * (HD / 4); e += S_THR) {
+          const int r = e / (HD / 4), c = e % (HD / 4) * 4;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (j0 + r < item_keys) {
+            const long long row = paged_row(io, p, s.seq, w.head, s.key0 + j0 + r);
+            if (row >= 0) v = load4((const T *)pages + row * HD + c);
+          }
+          *reinterpret_cast<float4 *>(&KVs[r * LD + c]) = v;
+        }
+      };
+      __syncthreads();
+      load_tile(io.k_pages);
+      __syncthreads();
+      float sc[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < HD; d += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = *reinterpret_cast<const float4 *>(&Qs[(ty * 4 + i) * LD + d]);
+          b[i] = *reinterpret_cast<const float4 *>(&KVs[(tx + 16 * i) * LD + d]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sc[i][j] = fmaf(a[i].x, b[j].x, sc[i][j]);
+            sc[i][j] = fmaf(a[i].y, b[j].y, sc[i][j]);
+            sc[i][j] = fmaf(a[i].z, b[j].z, sc[i][j]);
+            sc[i][j] = fmaf(a[i].w, b[j].w, sc[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float mt = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sc[i][j] = j0 + tx + 16 * j < lim[i] ? sc[i][j] * sl2 : -INFINITY;
+          mt = fmaxf(mt, sc[i][j]);
+        }
+#pragma unroll
+        for (int b = 8; b > 0; b >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, b));
+        const float mn = fmaxf(m[i], mt), base = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(m[i] - base);
+        m[i] = mn;
+        float ps = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = exp2f(sc[i][j] - base);
+          ps += e;
+          Ps[(ty * 4 + i) * LP + tx + 16 * j] = e;
+        }
+#pragma unroll
+        for (int b = 8; b > 0; b >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, b);
+        l[i] = l[i] * f + ps;
+#pragma unroll
+        for (int d = 0; d < DPT; ++d) o[i][d] *= f;
+      }
+      __syncthreads();
+      load_tile(io.v_pages);
+      __syncthreads();
+#pragma unroll 2
+      for (int k = 0; k < S_KT; k += 4) {
+        float4 pr[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          pr[i] = *reinterpret_cast<const float4 *>(&Ps[(ty * 4 + i) * LP + k]);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          float v[DPT];
+#pragma unroll
+          for (int x = 0; x < NV; ++x)
+#pragma unroll
+            for (int y = 0; y < VEC; ++y) v[x * VEC + y] = KVs[(k + kk) * LD + x * 16 * VEC + tx * VEC + y];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float pv = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
+#pragma unroll
+            for (int d = 0; d < DPT; ++d) o[i][d] = fmaf(pv, v[d], o[i][d]);
+          }
+        }
+      }
+    }
+    const PagedDest dest = paged_dest(p, io, w, blockIdx.x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      if (r >= rows) continue;
+      const int tok = s.tok0 + i0 + r / rep, h = w.head * rep + r % rep;
+      if (dest.kind == PAGED_OUT) {
+        const float il = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        T *dst = (T *)io.out + ((size_t)tok * io.Hq + h) * HD;
+#pragma unroll
+        for (int d = 0; d < DPT; ++d)
+          dst[d / VEC * 16 * VEC + tx * VEC + d % VEC] = from_f<T>(o[i][d] * il);
+      } else {
+        const size_t row = paged_part_row(p, io, dest, r, tok, h);
+#pragma unroll
+        for (int d = 0; d < DPT; ++d)
+          io.part_o[row * HD + d / VEC * 16 * VEC + tx * VEC + d % VEC] = o[i][d];
+        if (tx == 0) {
+          io.part_ml[row] = make_float2(m[i], l[i]);
+          if (dest.redirect) paged_redirect(p, io, dest, blockIdx.x, tok, h);
+        }
+      }
+    }
+  }
+}
+
+// ---- joining ------------------------------------------------------------------------------------
+
+// A row's running state while its partial results are folded in, one warp per row; lane i holds
+// columns i V .. i V + V - 1.
+template <int HD>
+struct Fold {
+  static constexpr int V = HD / 32;
+  float m = -INFINITY, l = 0.f, acc[V];
+  __device__ Fold() {
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  }
+  // n partial results, lane i of `ml` holding the i-th's (m, l), `row` its row in part_o.
+  __device__ __forceinline__ void add(const float *__restrict__ part_o, int n, float2 ml,
+                                      size_t row) {
+    const int lane = threadIdx.x & 31;
+    const float mn = fmaxf(m, warp_max(lane < n ? ml.x : -INFINITY));
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float f = exp2f(m - base);
+    const float c = lane < n ? exp2f(ml.x - base) : 0.f;
+    m = mn;
+    l = l * f + warp_sum(lane < n ? c * ml.y : 0.f);
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= f;
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      float x[4][V];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const size_t r = __shfl_sync(0xffffffffu, row, min(i0 + i, n - 1));
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[i][v] = i0 + i < n ? part_o[r * HD + lane * V + v] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float ci = __shfl_sync(0xffffffffu, c, (i0 + i) & 31);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = i0 + i < n ? fmaf(x[i][v], ci, acc[v]) : acc[v];
+      }
+    }
+  }
+  // Row r of the item whose pieces lie in CTAs first .. last (the item begins in `first`).
+  __device__ __forceinline__ void add_pieces(const PagedIO &io, int first, int last, int r) {
+    const int lane = threadIdx.x & 31;
+    for (int c0 = first; c0 <= last; c0 += 32) {
+      const int n = min(32, last - c0 + 1);
+      const int c = c0 + min(lane, n - 1);
+      const size_t row = paged_slot_row(io, c, c == first, r);
+      add(io.part_o, n, io.part_ml[row], row);
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T *dst) const {
+    const float il = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) dst[(threadIdx.x & 31) * V + v] = from_f<T>(acc[v] * il);
+  }
+};
+
+// Joins the items that a range boundary cuts: block x looks at the boundary before CTA x + 1, and
+// acts where that is the first boundary inside its item.  A warp per row.
+template <typename T, int HD>
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedIO io) {
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x + 1;
+  const PagedHead h = io.heads[c];
+  if (!h.joins) return;
+  const int rows = h.tokens * io.rep;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
+    Fold<HD> f;
+    f.add_pieces(io, c - 1, h.last, r);
+    f.store((T *)io.out +
+            ((size_t)(h.tok0 + r / io.rep) * io.Hq + h.head * io.rep + r % io.rep) * HD);
+  }
+}
+
+// Joins each row's result over the shared prefix with the one over its own keys; either may have
+// been cut into pieces.  A block per packed row, a warp per query head.
+template <typename T, int HD>
+__global__ void __launch_bounds__(256) paged_join_prefix_kernel(PagedShape p, PagedIO io) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ int live;
+  const int tok = blockIdx.x;
+  if (threadIdx.x == 0) {
+    // the sequence that holds this row, if it is one the attention took
+    int lo = 0, hi = p.n_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (p.seq_off[mid] <= tok) lo = mid;
+      else hi = mid;
+    }
+    const PagedSeg s = paged_seg(p, lo + 1);
+    live = s.n > 0 && tok >= s.tok0 && tok < s.tok0 + s.n;
+  }
+  __syncthreads();
+  if (!live) return;
+  for (int h = threadIdx.x >> 5; h < io.Hq; h += 8) {
+    Fold<HD> f;
+    for (int which = 0; which < 2; ++which) {
+      const size_t row = paged_region_row(p, io, which, tok, h);
+      const float2 ml = io.part_ml[row];
+      if (ml.y < 0.f) {  // cut into pieces from this CTA on
+        const int c = __float_as_int(ml.x);
+        const PagedHead hd = io.heads[c + 1];
+        f.add_pieces(io, c, hd.last, (tok - hd.tok0) * io.rep + h % io.rep);
+      } else {
+        f.add(io.part_o, 1, ml, row);
+      }
+    }
+    f.store((T *)io.out + ((size_t)tok * io.Hq + h) * HD);
+  }
+}
+
+template <typename T, int HD>
+int run_simt(const PagedShape &p, const PagedIO &io, cudaStream_t s) {
+  note_launch(s, "paged_attn_simt");
+  cudaFuncSetAttribute(paged_attn_simt_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)simt_smem<HD>());
+  launch_pdl(paged_attn_simt_kernel<T, HD>, io.ctas, S_THR, simt_smem<HD>(), s, p, io);
+  return check_launch("paged_attn_simt");
+}
+
+template <typename T, int HD>
+int run_join(const PagedShape &p, const PagedIO &io, cudaStream_t s) {
+  if (p.shared_len > 0) {
+    note_launch(s, "paged_join_prefix");
+    launch_pdl(paged_join_prefix_kernel<T, HD>, p.n_tokens, 256, 0, s, p, io);
+    return check_launch("paged_join_prefix");
+  }
+  if (io.ctas < 2) return DG_OK;
+  note_launch(s, "paged_join");
+  launch_pdl(paged_join_kernel<T, HD>, dim3(io.ctas - 1, (io.rows + 31) / 32), 256, 0, s, io);
+  return check_launch("paged_join");
+}
+
+inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// Query rows per item, keys per tile and CTAs of the kernel that takes the call.
+void paged_tiling(const PagedCall &c, PagedShape *p, PagedIO *io) {
+  const int rep = c.Hq / c.Hkv;
+  const bool tc = paged_tc_supported(c.act, c.hd);
+  const int tile = tc ? PAGED_TC_ROWS : S_ROWS;
+  p->qt = tile / rep * (tc ? 2 : 1);
+  p->qn = tc ? tile / rep : 0;
+  p->kt = tc ? PAGED_TC_KT : S_KT;
+  io->rows = p->qt * rep;
+  const long long most = (long long)c.n_tokens * rep;
+  if (io->rows > most) io->rows = (int)most;
+  io->ctas = num_sms() * (tc ? 1 : 2);
+}
+
+struct PagedLayout {
+  size_t heads, part_o, part_ml, total;
+};
+PagedLayout paged_layout(const PagedCall &c) {
+  PagedShape p{};
+  PagedIO io{};
+  paged_tiling(c, &p, &io);
+  const size_t rows = (size_t)2 * io.ctas * io.rows +
+                      (c.shared_len > 0 ? (size_t)2 * c.n_tokens * c.Hq : 0);
+  PagedLayout l;
+  l.heads = 0;
+  l.part_ml = up256(io.ctas * sizeof(PagedHead));
+  l.part_o = l.part_ml + up256(rows * sizeof(float2));
+  l.total = l.part_o + up256(rows * c.hd * sizeof(float));
+  return l;
+}
+
+}  // namespace
+
+bool paged_attn_supported(int act, int Hq, int Hkv, int hd) {
+  return Hq / Hkv <= S_ROWS && (hd == 32 || hd == 64 || hd == 128);
+}
+
+size_t paged_attn_ws_bytes(const PagedCall &c) { return paged_layout(c).total; }
+
+int launch_paged_attn(const PagedCall &c, void *ws, cudaStream_t s) {
+  PagedShape p{};
+  PagedIO io{};
+  paged_tiling(c, &p, &io);
+  const PagedLayout l = paged_layout(c);
+  p.seq_off = c.seq_off;
+  p.kv_len = c.kv_len;
+  p.n_seqs = c.n_seqs;
+  p.n_tokens = c.n_tokens;
+  p.Hkv = c.Hkv;
+  p.causal = c.causal;
+  p.shared_len = c.shared_len;
+  p.cap = c.max_pages * c.page_size;
+  io.q = c.q;
+  io.out = c.out;
+  io.k_pages = c.k_pages;
+  io.v_pages = c.v_pages;
+  io.page_table = c.page_table;
+  io.n_pages = c.n_pages;
+  io.max_pages = c.max_pages;
+  io.page_shift = 0;
+  while ((1 << io.page_shift) < c.page_size) ++io.page_shift;
+  io.Hq = c.Hq;
+  io.rep = c.Hq / c.Hkv;
+  io.heads = (PagedHead *)((char *)ws + l.heads);
+  io.part_ml = (float2 *)((char *)ws + l.part_ml);
+  io.part_o = (float *)((char *)ws + l.part_o);
+  io.status = c.status;
+  int rc = DG_ERR_UNSUPPORTED;
+#define DG_PAGED_CASE(T, HD)              \
+  {                                       \
+    rc = run_simt<T, HD>(p, io, s);       \
+    if (rc == DG_OK) rc = run_join<T, HD>(p, io, s); \
+  }
+  if (c.act == DG_F32) {
+    if (c.hd == 32) DG_PAGED_CASE(float, 32)
+    else if (c.hd == 64) DG_PAGED_CASE(float, 64)
+    else DG_PAGED_CASE(float, 128)
+  } else {
+    if (c.hd == 32) DG_PAGED_CASE(bf16, 32)
+    else if (c.hd == 64) DG_PAGED_CASE(bf16, 64)
+    else DG_PAGED_CASE(bf16, 128)
+  }
+#undef DG_PAGED_CASE
+  return rc;
+}
+
+}  // namespace dg

@@ -383,6 +383,107 @@ int dg_generate(const dg_config *cfg, const dg_model *model, int batch, int32_t 
                 int32_t *cache_len, int cache_cap, int append, void *ws, size_t ws_bytes,
                 int32_t *dev_status, void *stream);
 
+/* ---- paged K/V cache ---------------------------------------------------------------------- */
+
+/* Sequences of different lengths on one cache whose rows lie in pages ("DiffusionGemma Technical
+ * Report", Figure 4: a causally encoded cache that canvases attend to; "Limits and open work":
+ * serving diffusion and autoregressive requests together).  The pages of the method give no cache
+ * layout; these calls are the library's.
+ *
+ * Packed rows: the new tokens of n_seqs sequences stand one behind another; sequence s holds rows
+ *   [seq_off[s], seq_off[s + 1]) (device int32 [n_seqs + 1], ascending; empty sequences allowed).
+ *   n_tokens is the number of rows the buffers hold; rows from seq_off[n_seqs] on are left as they
+ *   were, so that a batch may be padded (and a captured call replayed with other offsets).
+ * Lengths: kv_len[s] (device int32) counts the keys sequence s had before its new tokens, so new
+ *   token i stands at position kv_len[s] + i.  No call changes it: add the new tokens after the last
+ *   layer.
+ * Errors the device sees: offsets or lengths that are negative, not ascending or past n_tokens, and
+ *   page ids outside [0, n_pages), record DG_ERR_INVALID_ARG; a sequence whose keys would pass
+ *   max_pages * page_size records DG_ERR_CAPACITY.  Such a sequence is skipped (its output rows and
+ *   pages are left as they were), except that a bad page id among an attention's keys leaves that
+ *   sequence's output rows (with a shared prefix, if the page is one of the prefix: every row)
+ *   without meaning.  Nothing is read or written out of range. */
+
+/* One layer's pages (HOST struct).  Key j of sequence s is row j % page_size of page
+ * page_table[s][j / page_size]; entries behind a sequence's last key are not read.  What stands
+ * in a page behind its last key never reaches a result, whatever it is. */
+typedef struct dg_paged_kv {
+  void *k_pages, *v_pages;     /* [n_pages][Hkv][page_size][hd], activation type, 16-byte aligned */
+  const int32_t *page_table;   /* device int32 [n_seqs][max_pages] */
+  int32_t n_pages;             /* n_pages * Hkv * page_size < 2^31 */
+  int32_t page_size;           /* a power of two, 16 .. 1024 */
+  int32_t max_pages;
+} dg_paged_kv;
+
+/* Rotary positions: pair j of the first rot_dim elements of a head turns by position * f_j,
+ * f_j = rope_theta^(-2j / rot_dim), the elements behind them pass unrotated.
+ *   layout   DG_ROPE_HALF: pairs (j, j + rot_dim / 2);  DG_ROPE_INTERLEAVED: pairs (2j, 2j + 1)
+ *   scaling  DG_ROPE_UNSCALED;
+ *            DG_ROPE_LINEAR: f_j / factor (position interpolation);
+ *            DG_ROPE_BY_PARTS: f_j / factor * (1 - r_j) + f_j * r_j, with r_j = (t_j - beta_slow) /
+ *            (beta_fast - beta_slow) clamped to [0, 1] and t_j = orig_len * f_j / 2 pi the turns of
+ *            pair j over the original context ("NTK-by-parts": Peng et al., 2023, "YaRN")
+ *   mscale   multiplies cosines and sines (1: none)
+ * A null dg_rope is DG_ROPE_HALF over the whole head, unscaled (what dg_kv_append uses). */
+enum { DG_ROPE_HALF = 0, DG_ROPE_INTERLEAVED = 1 };
+enum { DG_ROPE_UNSCALED = 0, DG_ROPE_LINEAR = 1, DG_ROPE_BY_PARTS = 2 };
+typedef struct dg_rope {
+  int32_t rot_dim;             /* a multiple of 16, 0 .. head_dim (0: no rotation) */
+  int32_t layout, scaling;
+  double factor;               /* > 0; read by LINEAR and BY_PARTS */
+  double orig_len, beta_slow, beta_fast;   /* > 0; 0 <= beta_slow < beta_fast; read by BY_PARTS */
+  double mscale;
+} dg_rope;
+
+/* Per-head RMSNorm of queries and keys, the rotation and the head split of projected rows, in one
+ * pass: what stands between a QKV projection and dg_canvas_attn.
+ *   qkv [batch * n_tokens] rows of (Hq + 2 Hkv) hd elements (q heads, k heads, v heads) in the
+ *   activation type, ld_qkv elements apart (ld_qkv * element size a multiple of 16 bytes).
+ *   For each q and k head x:  y = x / sqrt(mean(x^2) + rms_eps) * gain, then the rotation at
+ *   position cache_len[b] + i; computed in fp32 (angles in fp64), rounded once.  v is copied.
+ *   q_gain, k_gain: fp32 [hd], or NULL: that side is not normed.
+ *   q [batch][n_tokens][Hq][hd], k_new, v_new [batch][Hkv][n_tokens][hd].
+ * 16-byte aligned tensors; outputs may not overlap qkv. */
+int dg_qk_norm_rope(const dg_config *cfg, int batch, int n_tokens, const void *qkv,
+                    long long ld_qkv, const int32_t *cache_len, const float *q_gain,
+                    const float *k_gain, const dg_rope *rope, void *q, void *k_new, void *v_new,
+                    int32_t *dev_status, void *stream);
+
+/* The same for packed rows, with K and V written straight to their pages: row i of sequence s goes
+ * to key kv_len[s] + i.  q [n_tokens][Hq][hd], or NULL where only the cache is filled.  A sequence
+ * that does not fit its pages, or a row whose page id is bad, still gets its q. */
+int dg_paged_append(const dg_config *cfg, int n_seqs, int n_tokens, const int32_t *seq_off,
+                    const int32_t *kv_len, const void *qkv, long long ld_qkv, const float *q_gain,
+                    const float *k_gain, const dg_rope *rope, const dg_paged_kv *kv, void *q,
+                    int32_t *dev_status, void *stream);
+
+/* Bytes of scratch of the two attention calls below for n_tokens packed rows, on the current device;
+ * shared_len: as given to dg_prefix_attn, 0 for dg_paged_attn.  0 on invalid arguments. */
+size_t dg_paged_workspace_size(const dg_config *cfg, int n_seqs, int n_tokens, int shared_len);
+
+/* Attention of packed sequences over their pages, the new tokens' K and V already appended: for row i
+ * of sequence s and query head h (kv head h / (Hq / Hkv)),
+ *   o = softmax(q K^T / sqrt(hd)) V over keys [0, kv_len[s] + n_s) (causal = 0: a canvas) or
+ *   [0, kv_len[s] + i] (causal = 1: a prompt, a chunk of one, or a single next token).
+ *   q, out [n_tokens][Hq][hd].  out may not overlap q.
+ * Scores, softmax statistics and sums are fp32.  Hq / Hkv <= 64 (DG_ERR_UNSUPPORTED otherwise).
+ * The values of keys a sequence holds must be finite, those of later tokens of its batch included: a
+ * non-finite value may reach the rows before it. */
+int dg_paged_attn(const dg_config *cfg, int n_seqs, int n_tokens, const int32_t *seq_off,
+                  const int32_t *kv_len, const void *q, const dg_paged_kv *kv, int causal,
+                  void *out, void *ws, size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/* dg_paged_attn for sequences that share their first shared_len keys (continuations or canvases of
+ * one long prompt): the keys of the prefix are read once for all rows instead of once for each
+ * sequence, and joined with each sequence's own.  shared_len: a multiple of page_size, > 0; the
+ * first shared_len / page_size entries of every page-table row name the same pages (those of row 0
+ * are read), and kv_len[s] >= shared_len for every sequence that has rows (DG_ERR_INVALID_ARG on
+ * the device otherwise).  Other arguments and results as dg_paged_attn. */
+int dg_prefix_attn(const dg_config *cfg, int n_seqs, int n_tokens, const int32_t *seq_off,
+                   const int32_t *kv_len, int shared_len, const void *q, const dg_paged_kv *kv,
+                   int causal, void *out, void *ws, size_t ws_bytes, int32_t *dev_status,
+                   void *stream);
+
 /* ---- fixed-scratch entry point ---------------------------------------------------------- */
 
 /* dg_logits_entropy for callers that cannot provide device scratch memory.  The pages have no
