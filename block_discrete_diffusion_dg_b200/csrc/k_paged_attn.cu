@@ -410,7 +410,7 @@ int launch_paged_attn(const PagedCall &c, void *ws, cudaStream_t s) {
   int rc = DG_ERR_UNSUPPORTED;
 #define DG_PAGED_CASE(T, HD)              \
   {                                       \
-    rc = run_simt<T, HD>(p, io, s);       \
+    rc = paged_tc_supported(c.act, HD) ? launch_paged_tc(c, p, io, s) : run_simt<T, HD>(p, io, s); \
     if (rc == DG_OK) rc = run_join<T, HD>(p, io, s); \
   }
   if (c.act == DG_F32) {

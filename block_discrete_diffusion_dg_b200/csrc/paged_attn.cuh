@@ -23,8 +23,11 @@ struct PagedIO {
   int32_t *status;
 };
 
+// Tensor-core kernel (k_paged_attn_tc.cu): query rows and keys per tile.
 constexpr int PAGED_TC_ROWS = 128, PAGED_TC_KT = 128;
-__host__ inline bool paged_tc_supported(int, int) { return false; }
+inline bool paged_tc_supported(int act, int hd) { return act == DG_BF16 && (hd == 64 || hd == 128); }
+struct PagedCall;
+int launch_paged_tc(const PagedCall &c, const PagedShape &p, const PagedIO &io, cudaStream_t s);
 
 // Row (of hd elements) of key `pos` of a sequence in the page pool, -1 (and the status word set)
 // for a page id outside it.
