@@ -49,11 +49,11 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(PagedShape p,
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   if (tid < 32) {
     int err;
-    const PagedStart st = paged_locate(p, blockIdx.x, gridDim.x, &err);
+    const PagedStart st = paged_locate(p, PAGED_WIDE, blockIdx.x, gridDim.x, &err);
     if (tid == 0) {
       start_s = st;
       if (blockIdx.x == 0) paged_report(io, err);
-      paged_write_head(p, io, st, blockIdx.x);
+      io.heads[blockIdx.x] = paged_head(p, PAGED_WIDE, st);
     }
   }
   __syncthreads();
@@ -61,11 +61,9 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(PagedShape p,
   const int rep = io.rep;
   const float sl2 = 1.4426950408889634f * rsqrtf((float)HD);
   PagedWalk w;
-  for (w.begin(p, st); w.more(); w.next(p)) {
+  for (w.begin(p, PAGED_WIDE, st); w.more(); w.next(p)) {
     const PagedSeg s = w.s;
-    const int k0 = w.k0(), k1 = w.k1();
-    const int i0 = w.item * p.qt, toks = paged_item_tokens(p, s, w.item), rows = toks * rep;
-    const int item_keys = paged_item_keys(p, s, w.item);
+    const int i0 = w.tok, toks = w.toks, rows = toks * rep, item_keys = w.keys;
     __syncthreads();  // the last piece's readers of Qs and KVs are done
     for (int e = tid; e < S_ROWS * (HD / 4); e += S_THR) {
       const int r = e / (HD / 4), c = e % (HD / 4) * 4;
@@ -86,7 +84,7 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(PagedShape p,
 #pragma unroll
       for (int d = 0; d < DPT; ++d) o[i][d] = 0.f;
     }
-    for (int t = k0; t < k1; ++t) {
+    for (int t = w.t0; t < w.t1; ++t) {
       const int j0 = t * S_KT;
       auto load_tile = [&](const void *pages) {
         for (int e = tid; e < S_KT * (HD / 4); e += S_THR) {
@@ -226,25 +224,28 @@ struct Fold {
     l = l * f + warp_sum(lane < n ? c * ml.y : 0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= f;
-    for (int i0 = 0; i0 < n; i0 += 4) {
-      float x[4][V];
+    constexpr int U = 8;   // rows in flight
+    for (int i0 = 0; i0 < n; i0 += U) {
+      float x[U][V];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < U; ++i) {
         const size_t r = __shfl_sync(0xffffffffu, row, min(i0 + i, n - 1));
 #pragma unroll
         for (int v = 0; v < V; ++v) x[i][v] = i0 + i < n ? part_o[r * HD + lane * V + v] : 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < U; ++i) {
         const float ci = __shfl_sync(0xffffffffu, c, (i0 + i) & 31);
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = i0 + i < n ? fmaf(x[i][v], ci, acc[v]) : acc[v];
       }
     }
   }
-  // Row r of the item whose pieces lie in CTAs first .. last (the item begins in `first`).
+  // Row r of the item whose pieces lie with workers first .. last (the item begins at `first`).
+  // (`last` counted within their kind).
   __device__ __forceinline__ void add_pieces(const PagedIO &io, int first, int last, int r) {
     const int lane = threadIdx.x & 31;
+    last += paged_first_worker(io, paged_worker_kind(io, first));
     for (int c0 = first; c0 <= last; c0 += 32) {
       const int n = min(32, last - c0 + 1);
       const int c = c0 + min(lane, n - 1);
@@ -260,17 +261,35 @@ struct Fold {
   }
 };
 
-// Joins the items that a range boundary cuts: block x looks at the boundary before CTA x + 1, and
-// acts where that is the first boundary inside its item.  A warp per row.
+// Joins the items that range boundaries cut: worker c acts where it is the second to work on the item
+// that its range begins in.  A warp per row; a block takes one worker and a share of its rows (the
+// first `blocks` of them: wide items 8 shares, narrow ones 1), or eight workers of few-row items.
+struct JoinGrid {
+  int wide, narrow, few;   // blocks
+};
 template <typename T, int HD>
-__global__ void __launch_bounds__(256) paged_join_kernel(PagedIO io) {
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedIO io, JoinGrid g) {
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x + 1;
+  const int warp = threadIdx.x >> 5;
+  int b = blockIdx.x, c, r, step;
+  if (b < g.wide) {
+    c = b / 8;
+    r = b % 8 * 8 + warp;
+    step = 64;
+  } else if ((b -= g.wide) < g.narrow) {
+    c = io.ctas + b;
+    r = warp;
+    step = 8;
+  } else {
+    c = 3 * io.ctas + (b - g.narrow) * 8 + warp;
+    r = 0;
+    step = 1;
+  }
   const PagedHead h = io.heads[c];
   if (!h.joins) return;
   const int rows = h.tokens * io.rep;
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
+  for (; r < rows; r += step) {
     Fold<HD> f;
     f.add_pieces(io, c - 1, h.last, r);
     f.store((T *)io.out +
@@ -304,7 +323,7 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(PagedShape p, Pa
     for (int which = 0; which < 2; ++which) {
       const size_t row = paged_region_row(p, io, which, tok, h);
       const float2 ml = io.part_ml[row];
-      if (ml.y < 0.f) {  // cut into pieces from this CTA on
+      if (ml.y < 0.f) {  // cut into pieces from this worker on
         const int c = __float_as_int(ml.x);
         const PagedHead hd = io.heads[c + 1];
         f.add_pieces(io, c, hd.last, (tok - hd.tok0) * io.rep + h % io.rep);
@@ -332,40 +351,50 @@ int run_join(const PagedShape &p, const PagedIO &io, cudaStream_t s) {
     launch_pdl(paged_join_prefix_kernel<T, HD>, p.n_tokens, 256, 0, s, p, io);
     return check_launch("paged_join_prefix");
   }
-  if (io.ctas < 2) return DG_OK;
+  // no item of a kind can exist with fewer rows than it takes
+  JoinGrid g{0, 0, 0};
+  if (p.n_tokens > p.qn) g.wide = 8 * io.ctas;
+  if (p.qn > 0 && p.n_tokens > p.qf) g.narrow = 2 * io.ctas;
+  if (p.qf > 0) g.few = io.ctas;
   note_launch(s, "paged_join");
-  launch_pdl(paged_join_kernel<T, HD>, dim3(io.ctas - 1, (io.rows + 31) / 32), 256, 0, s, io);
+  launch_pdl(paged_join_kernel<T, HD>, g.wide + g.narrow + g.few, 256, 0, s, io, g);
   return check_launch("paged_join");
 }
 
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// Query rows per item, keys per tile and CTAs of the kernel that takes the call.
+// Query rows per item, keys per tile and workers of the kernel that takes the call.
 void paged_tiling(const PagedCall &c, PagedShape *p, PagedIO *io) {
   const int rep = c.Hq / c.Hkv;
   const bool tc = paged_tc_supported(c.act, c.hd);
   const int tile = tc ? PAGED_TC_ROWS : S_ROWS;
   p->qt = tile / rep * (tc ? 2 : 1);
   p->qn = tc ? tile / rep : 0;
-  p->kt = tc ? PAGED_TC_KT : S_KT;
-  io->rows = p->qt * rep;
-  const long long most = (long long)c.n_tokens * rep;
-  if (io->rows > most) io->rows = (int)most;
+  p->qf = tc ? PAGED_TC_FEW / rep : 0;
+  p->kt[PAGED_WIDE] = p->kt[PAGED_NARROW] = tc ? PAGED_TC_KT : S_KT;
+  p->kt[PAGED_FEW] = PAGED_TC_FEW_KT;
+  p->start_cost[PAGED_WIDE] = tc ? PAGED_TC_START_WIDE : 0;
+  p->start_cost[PAGED_NARROW] = PAGED_TC_START_NARROW;
+  p->start_cost[PAGED_FEW] = PAGED_TC_START_FEW;
   io->ctas = num_sms() * (tc ? 1 : 2);
+  p->least[PAGED_FEW] = PAGED_TC_LEAST_FEW;
+  io->workers = tc ? 11 * io->ctas : io->ctas;
+  const long long most = (long long)c.n_tokens * rep;
+  for (int k = 0; k < 3; ++k) {
+    const int rows = (k == PAGED_WIDE ? p->qt : k == PAGED_NARROW ? p->qn : p->qf) * rep;
+    io->rows[k] = rows > most ? (int)most : rows;
+  }
+  io->region = tc ? paged_slot_row(*io, io->workers, false, 0) : (size_t)2 * io->ctas * io->rows[0];
 }
 
 struct PagedLayout {
   size_t heads, part_o, part_ml, total;
 };
-PagedLayout paged_layout(const PagedCall &c) {
-  PagedShape p{};
-  PagedIO io{};
-  paged_tiling(c, &p, &io);
-  const size_t rows = (size_t)2 * io.ctas * io.rows +
-                      (c.shared_len > 0 ? (size_t)2 * c.n_tokens * c.Hq : 0);
+PagedLayout paged_layout(const PagedCall &c, const PagedIO &io) {
+  const size_t rows = io.region + (c.shared_len > 0 ? (size_t)2 * c.n_tokens * c.Hq : 0);
   PagedLayout l;
   l.heads = 0;
-  l.part_ml = up256(io.ctas * sizeof(PagedHead));
+  l.part_ml = up256(io.workers * sizeof(PagedHead));
   l.part_o = l.part_ml + up256(rows * sizeof(float2));
   l.total = l.part_o + up256(rows * c.hd * sizeof(float));
   return l;
@@ -377,13 +406,18 @@ bool paged_attn_supported(int act, int Hq, int Hkv, int hd) {
   return Hq / Hkv <= S_ROWS && (hd == 32 || hd == 64 || hd == 128);
 }
 
-size_t paged_attn_ws_bytes(const PagedCall &c) { return paged_layout(c).total; }
+size_t paged_attn_ws_bytes(const PagedCall &c) {
+  PagedShape p{};
+  PagedIO io{};
+  paged_tiling(c, &p, &io);
+  return paged_layout(c, io).total;
+}
 
 int launch_paged_attn(const PagedCall &c, void *ws, cudaStream_t s) {
   PagedShape p{};
   PagedIO io{};
   paged_tiling(c, &p, &io);
-  const PagedLayout l = paged_layout(c);
+  const PagedLayout l = paged_layout(c, io);
   p.seq_off = c.seq_off;
   p.kv_len = c.kv_len;
   p.n_seqs = c.n_seqs;

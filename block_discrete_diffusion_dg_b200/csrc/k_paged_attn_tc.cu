@@ -4,13 +4,17 @@
 //
 // Query rows are token-major: row r of a tile is token r / rep, head r % rep of one kv head's group,
 // so every K/V tile is read once per group and any group size fits a tile of 128 rows.  One CTA per
-// SM walks its range of work; an item is
-//   wide    two query tiles A and B (up to 256 rows) against the same key tiles, or
-//   narrow  one query tile (up to 128 rows: single tokens, short prompts) whose even key tiles go
-//           through chain A and odd ones through chain B, joined at the end,
-// so that both chains always work and one's softmax overlaps the other's matrix products:
+// SM runs two chains of
 //   S_x = Q_x K^T    (128 x 128 keys x head_dim, bf16 from shared memory)
-//   O_x += P_x V     (128 x head_dim x 128 keys, P from tensor memory, V from shared memory)
+//   P_x = softmax's numerators, O_x += P_x V    (P from tensor memory, V from shared memory)
+// so that the softmax of one overlaps the matrix products of the other:
+//   wide items     both chains take one query tile each (up to 256 rows) against the same key tiles;
+//   narrow items   (short prompts, tails: up to 128 rows) each chain walks a range of its own, so that
+//                  the start and end of one's items hide behind the other's work.
+// Few-row items (single tokens: up to 16 rows) would leave 7/8 of such a tile empty and pass each key
+// tile through a chain of four waits; there each of the eight softmax warps walks a range of its own
+// with mma.sync, 16 keys a step, from a ring of its own in the memory that the chains have left, so
+// that almost all of it is in flight: these items are bound by the bytes of their keys.
 // Tensor memory (512 columns): S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512); P_x is
 // written over S_x.  MMAs of one thread execute in issue order, so S_x of the next key tile is
 // issued right behind P_x V.
@@ -41,18 +45,23 @@ constexpr int P_HALF = 128 * 128;          // 128 rows of 64 bf16 (128-byte rows
 constexpr uint32_t P_COL_S = 0, P_COL_O = 256, P_TMEM = 512;
 constexpr float P_RESCALE = 8.f;           // log2 of the largest P between rescales
 constexpr unsigned FULL = 0xffffffffu;
+constexpr int P_STAGE = 32 * 32 * 4;       // a softmax warp's 32 rows x 32 columns on their way out
 // Registers per thread at launch, and after the split between the copy / MMA warpgroup (LO) and the
 // two softmax warpgroups (HI), which hold a whole row of S.
 constexpr int P_REGS = 168, P_REGS_LO = 104, P_REGS_HI = 200;
 static_assert(128 * P_REGS_LO + 256 * P_REGS_HI <= P_THR * P_REGS, "register split");
 static_assert(P_THR * P_REGS <= 65536, "launch registers");
 
+constexpr int F_KT = PAGED_TC_FEW_KT;      // few-row items: keys per step,
+constexpr int F_SLOTS = 6;                 // K and V slots of a warp's ring (three steps)
+
 template <int HD>
 struct Tc {
   static constexpr int HALVES = HD / 64;
   static constexpr int TILE = HALVES * P_HALF;          // 128 rows x HD
-  static constexpr int STAGES = HD == 128 ? 5 : 10;     // key and value tiles in flight
-  static constexpr size_t SMEM = 1024 + (size_t)TILE * (2 + STAGES) + 2048;
+  static constexpr int STAGES = HD == 128 ? 4 : 8;      // key and value tiles in flight
+  static_assert(8 * F_SLOTS * F_KT * HD * 2 <= (2 + STAGES) * TILE, "few-row rings");
+  static constexpr size_t SMEM = 1024 + (size_t)TILE * (2 + STAGES) + 8 * P_STAGE + 1024;
 };
 
 template <int R>
@@ -74,6 +83,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], const void *p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(tc::smem_u32(p))
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], const void *p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(tc::smem_u32(p))
+               : "memory");
+}
+// D += A B, m16n8k16, bf16 operands, fp32 accumulator.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 // 3-D tiled load of the box at (x = element, y, z).
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int x,
                                             int y, int z) {
@@ -93,152 +123,198 @@ __device__ __forceinline__ void p_fail(int32_t *st, volatile int *abort_flag) {
   *abort_flag = 1;
 }
 
-// One piece of a walk in terms of key tiles: tiles [t0, t1) of an item of `keys` keys.
-struct Piece {
-  bool narrow;
-  int t0, t1, keys, toks, i0;
-  __device__ __forceinline__ Piece(const PagedShape &p, const PagedWalk &w) {
-    toks = paged_item_tokens(p, w.s, w.item);
-    narrow = toks <= p.qn;
-    keys = paged_item_keys(p, w.s, w.item);
-    i0 = w.item * p.qt;
-    t0 = narrow ? 2 * w.k0() : w.k0();
-    t1 = narrow ? min(2 * w.k1(), (keys + PAGED_TC_KT - 1) / PAGED_TC_KT) : w.k1();
-  }
-};
-
 template <int HD>
 __global__ void __launch_bounds__(P_THR, 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV,
+                         const __grid_constant__ CUtensorMap tmKf,
+                         const __grid_constant__ CUtensorMap tmVf,
                          const __grid_constant__ PagedShape p, const __grid_constant__ PagedIO io) {
   pdl_wait();
   pdl_trigger();
   using namespace tc;
   using C = Tc<HD>;
-  constexpr int S = C::STAGES, TILE = C::TILE, HALVES = C::HALVES;
+  constexpr int S = C::STAGES, TILE = C::TILE, HALVES = C::HALVES, KT = PAGED_TC_KT;
   extern __shared__ uint8_t p_smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)p_smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t *sQ = smem;                                   // [2][TILE]
+  uint8_t *sQ = smem;                                   // [2][TILE], by chain
   uint8_t *sKV = sQ + 2 * TILE;                         // [S][TILE], K and V tiles in turn
-  uint64_t *q_full = reinterpret_cast<uint64_t *>(sKV + S * TILE);   // [2]
+  uint8_t *sOut = sKV + S * TILE;                       // [8][P_STAGE], by softmax warp
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(sOut + 8 * P_STAGE);   // [2]
   uint64_t *q_empty = q_full + 2, *full = q_empty + 2, *empty = full + S;
   uint64_t *s_full = empty + S, *p_full = s_full + 2, *pv_done = p_full + 2, *o_empty = pv_done + 2;
-  uint64_t *b_done = o_empty + 2, *mma_fin = b_done + 1;
-  float2 *b_ml = reinterpret_cast<float2 *>(mma_fin + 1);            // [128] (m, l) of chain B
-  PagedStart *start = reinterpret_cast<PagedStart *>(b_ml + 128);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
+  uint64_t *mma_fin = o_empty + 2;
+  uint64_t *chains_done = mma_fin + 1, *f_full = chains_done + 1;        // [8][F_SLOTS]
+  PagedStart *start = reinterpret_cast<PagedStart *>(f_full + 8 * F_SLOTS);   // wide, chain A, chain B
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 3);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  static_assert((4 + 2 * S + 10 + 8 * F_SLOTS) * 8 + 3 * sizeof(PagedStart) + 8 <= 1024, "shared memory");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    int err;
-    const PagedStart st = paged_locate(p, blockIdx.x, gridDim.x, &err);
+  if (warp == 1) {
     if (lane == 0) {
-      *start = st;
-      if (blockIdx.x == 0) paged_report(io, err);
-      paged_write_head(p, io, st, blockIdx.x);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&q_full[x], 1);
+        mbar_init(&q_empty[x], 1);
+        mbar_init(&s_full[x], 1);
+        mbar_init(&p_full[x], 4);
+        mbar_init(&pv_done[x], 1);
+        mbar_init(&o_empty[x], 4);
+      }
+      for (int s = 0; s < S; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], 1);
+      }
+      mbar_init(mma_fin, 1);
+      mbar_init(chains_done, 8);
+      for (int i = 0; i < 8 * F_SLOTS; ++i) mbar_init(&f_full[i], 1);
+      *abort_flag = 0;
+      fence_mbar_init();
     }
-  } else if (warp == 1) {
+    __syncwarp();
     tmem_alloc(tmem_slot, P_TMEM);
     tmem_relinquish();
-  } else if (warp == 2 && lane == 0) {
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&q_full[x], 1);
-      mbar_init(&q_empty[x], 1);
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);
-      mbar_init(&pv_done[x], 1);
-      mbar_init(&o_empty[x], 4);
+  } else if (warp < 4) {
+    // warp 0 finds the range of wide items, warps 2 and 3 those of the chains' narrow items
+    const int kind = warp == 0 ? PAGED_WIDE : PAGED_NARROW;
+    const int worker = warp == 0 ? blockIdx.x : 2 * blockIdx.x + warp - 2;
+    int err;
+    const PagedStart st =
+        paged_locate(p, kind, worker, kind == PAGED_WIDE ? gridDim.x : 2 * gridDim.x, &err);
+    if (lane == 0) {
+      start[warp == 0 ? 0 : warp - 1] = st;
+      if (blockIdx.x == 0 && warp == 0) paged_report(io, err);
+      io.heads[paged_first_worker(io, kind) + worker] = paged_head(p, kind, st);
     }
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+  }
+  PagedStart few_start{};
+  if (warp >= 4) {
+    if (warp == 4 && lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      tma_prefetch_desc(&tmKf);
+      tma_prefetch_desc(&tmVf);
     }
-    mbar_init(b_done, 4);
-    mbar_init(mma_fin, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  } else if (warp == 3 && lane == 0) {
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    int err;
+    const int worker = 8 * blockIdx.x + warp - 4;
+    few_start = paged_locate(p, PAGED_FEW, worker, 8 * gridDim.x, &err);
+    if (lane == 0) io.heads[paged_first_worker(io, PAGED_FEW) + worker] = paged_head(p, PAGED_FEW, few_start);
   }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
-  const PagedStart st = *start;
   const int rep = io.rep, qn = p.qn;   // qn tokens of rep heads make a query tile
 
-  PagedWalk w;
   if (warp == 0) {
     // ---- copies
     reg_dec<P_REGS_LO>();
-    const int page = 1 << io.page_shift, box = min(page, PAGED_TC_KT);
-    uint32_t fill = 0, qs = 0;   // tiles and query tiles loaded so far
+    const int page = 1 << io.page_shift, box = min(page, KT);
+    uint32_t fill = 0, nq[2] = {0, 0};   // tiles and (by chain) query tiles loaded so far
     bool ok = true;
-    for (w.begin(p, st); ok && w.more(); w.next(p)) {
-      const Piece pc(p, w);
-      for (int x = 0; x < (pc.narrow ? 1 : 2) && ok; ++x, ++qs) {
-        const uint32_t b = qs & 1;
-        ok = __all_sync(FULL, mbar_wait(&q_empty[b], ((qs >> 1) & 1) ^ 1));
-        if (ok && lane == 0) {
-          mbar_expect_tx(&q_full[b], (uint32_t)(rep * qn * HD * 2));
-          for (int h = 0; h < HALVES; ++h)
-            tma_load_3d(sQ + b * TILE + h * P_HALF, &tmQ, &q_full[b], h * 64, w.head * rep,
-                        w.s.tok0 + pc.i0 + x * qn);
+    // the query tile of chain x: qn tokens from `tok` on
+    auto load_q = [&](const PagedWalk &w, int x, int tok) {
+      ok = __all_sync(FULL, mbar_wait(&q_empty[x], (nq[x] & 1) ^ 1) && !*abort_flag);
+      if (!ok) return;
+      if (lane == 0) {
+        mbar_expect_tx(&q_full[x], (uint32_t)(rep * qn * HD * 2));
+        for (int h = 0; h < HALVES; ++h)
+          tma_load_3d(sQ + x * TILE + h * P_HALF, &tmQ, &q_full[x], h * 64, w.head * rep,
+                      w.s.tok0 + tok);
+      }
+      ++nq[x];
+    };
+    // this lane's part of key tile t: keys [lane * box, lane * box + box); -1: none
+    auto lookup = [&](const PagedWalk &w, int t) -> int {
+      const int k = t * KT + lane * box;
+      if (lane * box >= KT || k >= w.keys) return -1;
+      const long long row = paged_row(io, p, w.s.seq, w.head, w.s.key0 + k);
+      return row < 0 ? io.n_pages * p.Hkv * page : (int)row;   // past the pool: reads zeros
+    };
+    auto load = [&](const CUtensorMap *tm, const PagedWalk &w, int t, int y) {
+      const int boxes = (min(KT, w.keys - t * KT) + box - 1) / box;
+      const uint32_t s = fill % S;
+      ok = __all_sync(FULL, mbar_wait(&empty[s], ((fill / S) & 1) ^ 1) && !*abort_flag);
+      if (!ok) return;
+      if (lane == 0) mbar_expect_tx(&full[s], (uint32_t)(boxes * box * HD * 2));
+      __syncwarp();
+      if (y >= 0) {
+        uint8_t *dst = sKV + s * TILE + lane * box * 128;
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) tma_load_2d(dst + h * P_HALF, tm, &full[s], h * 64, y);
+      }
+      ++fill;
+    };
+    // Tiles are loaded in the order in which the MMA warp releases them.
+    {
+      PagedWalk w;
+      for (w.begin(p, PAGED_WIDE, start[0]); ok && w.more(); w.next(p)) {
+        load_q(w, 0, w.tok);
+        if (ok) load_q(w, 1, w.tok + qn);
+        int y = lookup(w, w.t0);
+        for (int t = w.t0; t < w.t1 && ok; ++t) {
+          const int y_next = t + 1 < w.t1 ? lookup(w, t + 1) : -1;   // a tile ahead
+          load(&tmK, w, t, y);
+          if (ok) load(&tmV, w, t, y);
+          y = y_next;
         }
       }
-      // this lane's part of a tile: keys [lane * box, lane * box + box), its page looked up one
-      // tile ahead
-      auto lookup = [&](int t) -> int {
-        const int k = t * PAGED_TC_KT + lane * box;
-        if (t >= pc.t1 || lane * box >= PAGED_TC_KT || k >= pc.keys) return -1;
-        const int pos = w.s.key0 + k;
-        const long long row = paged_row(io, p, w.s.seq, w.head, pos);
-        return row < 0 ? io.n_pages * p.Hkv * page : (int)row;   // past the pool: reads zeros
+    }
+    {
+      PagedWalk w[2];
+      int t[2] = {0, 0}, y[2] = {0, 0};
+      auto load_k = [&](int x) {
+        if (!ok || !w[x].more()) return;
+        if (t[x] == w[x].t0) load_q(w[x], x, w[x].tok);
+        if (ok) load(&tmK, w[x], t[x], y[x]);
       };
-      int y = lookup(pc.t0);
-      for (int t = pc.t0; t < pc.t1 && ok; ++t) {
-        const int y_next = lookup(t + 1);
-        const int boxes = (min(PAGED_TC_KT, pc.keys - t * PAGED_TC_KT) + box - 1) / box;
-        for (int kv = 0; kv < 2 && ok; ++kv, ++fill) {
-          const uint32_t s = fill % S;
-          ok = __all_sync(FULL, mbar_wait(&empty[s], ((fill / S) & 1) ^ 1) && !*abort_flag);
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(&full[s], (uint32_t)(boxes * box * HD * 2));
-          __syncwarp();
-          if (y >= 0) {
-            const CUtensorMap *tm = kv ? &tmV : &tmK;
-            uint8_t *dst = sKV + s * TILE + lane * box * 128;
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h)
-              tma_load_2d(dst + h * P_HALF, tm, &full[s], h * 64, y);
+      for (int x = 0; x < 2; ++x) {
+        w[x].begin(p, PAGED_NARROW, start[1 + x]);
+        if (w[x].more()) y[x] = lookup(w[x], t[x] = w[x].t0);
+      }
+      load_k(0);
+      load_k(1);
+      while (ok && (w[0].more() || w[1].more())) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || !w[x].more()) continue;
+          load(&tmV, w[x], t[x], y[x]);
+          if (++t[x] == w[x].t1) {
+            w[x].next(p);
+            t[x] = w[x].t0;
           }
+          if (w[x].more()) y[x] = lookup(w[x], t[x]);
+          load_k(x);
         }
-        y = y_next;
       }
     }
     if (!ok && lane == 0) p_fail(io.status, abort_flag);
     // the copies in flight land before the CTA's shared memory can go away
     for (uint32_t f = fill > S ? fill - S : 0; f < fill; ++f) (void)mbar_wait(&full[f % S], (f / S) & 1);
-    for (uint32_t f = qs > 2 ? qs - 2 : 0; f < qs; ++f) (void)mbar_wait(&q_full[f & 1], (f >> 1) & 1);
+    for (int x = 0; x < 2; ++x)
+      if (nq[x] > 0) (void)mbar_wait(&q_full[x], (nq[x] - 1) & 1);
   } else if (warp == 1) {
     // ---- matrix products: the warp waits together, lane 0 issues
     reg_dec<P_REGS_LO>();
-    constexpr uint32_t id_s = idesc_bf16(128, PAGED_TC_KT), id_p = idesc_bf16_bmn(128, HD);
+    constexpr uint32_t id_s = idesc_bf16(128, KT), id_p = idesc_bf16_bmn(128, HD);
     const uint64_t dq = sdesc_sw128(sQ), dk = sdesc_sw128(sKV), dv = sdesc_sw128_mn(sKV, P_HALF);
-    uint32_t fill = 0, qs = 0, pieces = 0, pn[2] = {0, 0};
+    // by chain: pieces begun, key tiles whose P was taken
+    uint32_t pieces[2] = {0, 0}, pn[2] = {0, 0};
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       if (ok) ok = __all_sync(FULL, mbar_wait(bar, parity));
       fence_after();
     };
-    auto issue_s = [&](int x, uint32_t qb, uint32_t ks) {   // S_x = Q K^T
+    auto wait_fill = [&](uint32_t f) { wait(&full[f % S], (f / S) & 1); };
+    auto release = [&](uint64_t *bar) {
+      if (ok && lane == 0) commit(bar);
+    };
+    auto issue_s = [&](int x, uint32_t f) {   // S_x = Q_x K^T, K in fill f
       if (ok && lane == 0) {
-        const uint64_t ab = dq + (uint64_t)((qb * TILE) >> 4), bb = dk + (uint64_t)((ks * TILE) >> 4);
+        const uint64_t ab = dq + (uint64_t)((x * TILE) >> 4), bb = dk + (uint64_t)(((f % S) * TILE) >> 4);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * P_HALF) >> 4) + 2 * (kk & 3);
@@ -247,101 +323,103 @@ __global__ void __launch_bounds__(P_THR, 1)
         commit(&s_full[x]);
       }
     };
-    auto issue_pv = [&](int x, uint32_t vs, bool first) {   // O_x (+)= P_x V
+    // O_x (+)= P_x V, V in fill f: waits for P_x, and for O_x where it is begun anew
+    auto take_pv = [&](int x, uint32_t f, bool first) {
+      wait(&p_full[x], pn[x] & 1);
+      ++pn[x];
+      if (first && pieces[x] > 1) wait(&o_empty[x], pieces[x] & 1);   // of the piece before
       if (ok && lane == 0) {
-        const uint64_t bb = dv + (uint64_t)((vs * TILE) >> 4);
+        const uint64_t bb = dv + (uint64_t)(((f % S) * TILE) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < PAGED_TC_KT / 16; ++kk)
+        for (int kk = 0; kk < KT / 16; ++kk)
           mma_f16_ts(tmem + P_COL_O + x * 128, tmem + P_COL_S + x * 128 + kk * 8,
                      bb + (uint64_t)((kk * 16 * 128) >> 4), id_p, kk > 0 || !first ? 1u : 0u);
         commit(&pv_done[x]);
       }
     };
-    auto release = [&](uint64_t *bar) {
-      if (ok && lane == 0) commit(bar);
-    };
-    for (w.begin(p, st); ok && w.more(); w.next(p), ++pieces) {
-      const Piece pc(p, w);
-      const int N = pc.t1 - pc.t0;
-      const uint32_t f0 = fill;
-      auto k_at = [&](int i) { return f0 + 2 * (uint32_t)i; };       // fill number of K_i; V_i next
-      auto wait_fill = [&](uint32_t f) { wait(&full[f % S], (f / S) & 1); };
-      // V_i has landed; rows past the item's last key become zeros
-      auto wait_v = [&](int i) {
-        const uint32_t f = k_at(i) + 1;
-        wait_fill(f);
-        const int valid = pc.keys - (pc.t0 + i) * PAGED_TC_KT;
-        if (ok && valid < PAGED_TC_KT) {
-          uint8_t *base = sKV + (f % S) * TILE;
-          for (int e = lane; e < (PAGED_TC_KT - valid) * 8; e += 32)   // 8 chunks a row
+    // fill f (a value tile) has landed; rows past its `valid` keys become zeros
+    auto wait_v = [&](uint32_t f, int valid) {
+      wait_fill(f);
+      if (ok && valid < KT) {
+        uint8_t *base = sKV + (f % S) * TILE + valid * 128;
+        for (int e = lane; e < (KT - valid) * 8; e += 32)   // 8 chunks of 16 bytes a row
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h)
-              reinterpret_cast<uint4 *>(base + h * P_HALF + valid * 128)[e] = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
+          for (int h = 0; h < HALVES; ++h)
+            reinterpret_cast<uint4 *>(base + h * P_HALF)[e] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+    };
+    auto begin_q = [&](int x) {   // a piece of chain x: its query tile
+      wait(&q_full[x], pieces[x] & 1);
+      ++pieces[x];
+    };
+    uint32_t f = 0;   // fills taken so far (wide: the key tile whose S is issued next)
+    {
+      PagedWalk w;
+      for (w.begin(p, PAGED_WIDE, start[0]); ok && w.more(); w.next(p)) {
+        begin_q(0);
+        begin_q(1);
+        wait_fill(f);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          issue_s(x, f);
+          if (w.t0 + 1 == w.t1) release(&q_empty[x]);   // the piece's last S has read it
         }
-      };
-      const uint32_t qa = qs & 1;
-      wait(&q_full[qa], (qs >> 1) & 1);
-      if (!pc.narrow) wait(&q_full[qa ^ 1], ((qs + 1) >> 1) & 1);
-      const uint32_t qb = pc.narrow ? qa : qa ^ 1;
-      wait_fill(k_at(0));
-      issue_s(0, qa, k_at(0) % S);
-      // a query tile is free once the last S of the piece has read it
-      if (pc.narrow) {
-        release(&empty[k_at(0) % S]);
-        if (N == 1) release(&q_empty[qa]);
-        if (N > 1) {
-          wait_fill(k_at(1));
-          issue_s(1, qa, k_at(1) % S);
-          release(&empty[k_at(1) % S]);
-          if (N == 2) release(&q_empty[qa]);
-        }
-        for (int i = 0; i < N && ok; ++i) {
-          const int x = i & 1;
-          wait_v(i);
-          wait(&p_full[x], pn[x] & 1);
-          ++pn[x];
-          if (i < 2 && pieces > 0) wait(&o_empty[x], (pieces - 1) & 1);
-          issue_pv(x, (k_at(i) + 1) % S, i < 2);
-          release(&empty[(k_at(i) + 1) % S]);
-          if (i + 2 < N) {
-            wait_fill(k_at(i + 2));
-            issue_s(x, qa, k_at(i + 2) % S);
-            release(&empty[k_at(i + 2) % S]);
-            if (i + 3 == N) release(&q_empty[qa]);
-          }
-          if (__any_sync(FULL, *abort_flag != 0)) ok = false;
-        }
-        if (N == 1 && pieces > 0) wait(&o_empty[1], (pieces - 1) & 1);
-        qs += 1;
-      } else {
-        if (N == 1) release(&q_empty[qa]);
-        issue_s(1, qb, k_at(0) % S);
-        release(&empty[k_at(0) % S]);
-        if (N == 1) release(&q_empty[qb]);
-        for (int i = 0; i < N && ok; ++i) {
-          const bool more = i + 1 < N;
-          wait_v(i);
+        release(&empty[f % S]);
+        for (int t = w.t0; t < w.t1 && ok; ++t, f += 2) {
+          const bool more = t + 1 < w.t1;
+          wait_v(f + 1, w.keys - t * KT);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            wait(&p_full[x], pn[x] & 1);
-            ++pn[x];
-            if (i == 0 && pieces > 0) wait(&o_empty[x], (pieces - 1) & 1);
-            issue_pv(x, (k_at(i) + 1) % S, i == 0);
-            if (x == 1) release(&empty[(k_at(i) + 1) % S]);
+            take_pv(x, f + 1, t == w.t0);
+            if (x == 1) release(&empty[(f + 1) % S]);
             if (more) {
-              if (x == 0) wait_fill(k_at(i + 1));
-              issue_s(x, x ? qb : qa, k_at(i + 1) % S);
-              if (x == 1) release(&empty[k_at(i + 1) % S]);
-              if (i + 2 == N) release(&q_empty[x ? qb : qa]);
+              if (x == 0) wait_fill(f + 2);
+              issue_s(x, f + 2);
+              if (t + 2 == w.t1) release(&q_empty[x]);
+              if (x == 1) release(&empty[(f + 2) % S]);
             }
           }
           if (__any_sync(FULL, *abort_flag != 0)) ok = false;
         }
-        qs += 2;
       }
-      fill += 2 * (uint32_t)N;
+    }
+    {
+      PagedWalk w[2];
+      int t[2] = {0, 0};
+      auto next_s = [&](int x) {
+        if (t[x] == w[x].t0) begin_q(x);
+        wait_fill(f);
+        issue_s(x, f);
+        release(&empty[f % S]);
+        ++f;
+        if (t[x] + 1 == w[x].t1) release(&q_empty[x]);
+      };
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        w[x].begin(p, PAGED_NARROW, start[1 + x]);
+        if (w[x].more()) {
+          t[x] = w[x].t0;
+          next_s(x);
+        }
+      }
+      while (ok && (w[0].more() || w[1].more())) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || !w[x].more()) continue;
+          wait_v(f, w[x].keys - t[x] * KT);
+          take_pv(x, f, t[x] == w[x].t0);
+          release(&empty[f % S]);
+          ++f;
+          if (++t[x] == w[x].t1) {
+            w[x].next(p);
+            t[x] = w[x].t0;
+          }
+          if (w[x].more()) next_s(x);
+        }
+        if (__any_sync(FULL, *abort_flag != 0)) ok = false;
+      }
     }
     if (lane == 0) {
       if (!ok) p_fail(io.status, abort_flag);
@@ -360,185 +438,344 @@ __global__ void __launch_bounds__(P_THR, 1)
     const uint32_t lrow = (uint32_t)(q4 * 32) << 16;
     const uint32_t tS = tmem + lrow + P_COL_S + (uint32_t)x * 128;
     const uint32_t tO = tmem + lrow + P_COL_O + (uint32_t)x * 128;
+    float4 *stage = reinterpret_cast<float4 *>(sOut + (warp - 4) * P_STAGE);
     const float sl2 = 1.4426950408889634f / sqrtf((float)HD);
-    uint32_t ns = 0, pieces = 0, narrows = 0; // key tiles, pieces and narrow pieces so far
+    uint32_t ns = 0;                          // key tiles of this chain so far
     bool ok = true;
-    for (w.begin(p, st); w.more(); w.next(p), ++pieces) {
-      const Piece pc(p, w);
-      const int tile0 = pc.narrow ? 0 : x * qn;                 // first token of this chain's tile
-      const int toks = pc.narrow ? pc.toks : max(0, min(qn, pc.toks - tile0));
-      const int tl = tile0 + min(r / rep, max(toks, 1) - 1);    // this row's token in the item
-      const bool row_ok = r < toks * rep;
-      const bool warp_on = q4 * 32 < toks * rep;                // any row of this warp
-      const int seen = w.s.causal ? w.s.keys - w.s.n + pc.i0 + tl + 1 : pc.keys;
-      float m_use = -INFINITY, l = 0.f;
-      const int step = pc.narrow ? 2 : 1;
-      for (int t = pc.t0 + (pc.narrow ? x : 0); t < pc.t1; t += step, ++ns) {
-        if (__any_sync(FULL, *abort_flag != 0)) { ok = false; break; }
-        if (!__all_sync(FULL, mbar_wait(&s_full[x], ns & 1))) {
+    for (int kind = 0; kind < 2 && ok; ++kind) {
+      PagedWalk w;
+      for (w.begin(p, kind, start[kind == PAGED_WIDE ? 0 : 1 + x]); w.more(); w.next(p)) {
+        const int tile0 = kind == PAGED_WIDE ? x * qn : 0;        // first token of the chain's tile
+        const int rows = min(qn, w.toks - tile0) * rep;           // at least one token
+        const int tl = tile0 + min(r, rows - 1) / rep;            // this row's token in the item
+        const bool warp_on = q4 * 32 < rows;                      // any row of this warp
+        const int seen = w.s.causal ? w.s.keys - w.s.n + w.tok + tl + 1 : w.keys;
+        float m_use = -INFINITY, l = 0.f;
+        for (int t = w.t0; t < w.t1; ++t, ++ns) {
+          if (__any_sync(FULL, *abort_flag != 0)) { ok = false; break; }
+          if (!__all_sync(FULL, mbar_wait(&s_full[x], ns & 1))) {
+            p_fail(io.status, abort_flag);
+            ok = false;
+            break;
+          }
+          fence_after();
+          if (warp_on) {
+            const int lim = seen - t * KT;
+            // the row of S: two 64-column loads
+            uint32_t sa[64], sb[64];
+            tmem_ld64(tS, sa);
+            tmem_ld64(tS + 64, sb);
+            tmem_ld_wait64(sa);
+            tmem_ld_wait64(sb);
+            if (__any_sync(FULL, lim < KT)) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j) {
+                if (j >= lim) sa[j] = __float_as_uint(-INFINITY);
+                if (64 + j >= lim) sb[j] = __float_as_uint(-INFINITY);
+              }
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto fold_max = [&](const uint32_t (&v)[64]) {
+#pragma unroll
+              for (int j = 0; j < 64; j += 2)
+                m4[(j >> 1) & 3] =
+                    max3(m4[(j >> 1) & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+            };
+            fold_max(sa);
+            fold_max(sb);
+            const float m_new = fmaxf(m_use, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2);
+            // O is rescaled only when a row's maximum grew by more than 2^8 (P stays below 256, and
+            // O and l share their base, so O / l does not change); S of this tile was issued behind
+            // the last P V, so O includes it
+            if (__any_sync(FULL, m_use != -INFINITY && m_new > m_use + P_RESCALE)) {
+              const float g = m_use == -INFINITY ? 1.f : ex2(m_use - m_new);
+#pragma unroll 1
+              for (int c = 0; c < HD / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO + c * 32, o);
+                tmem_ld_wait(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * g);
+                tmem_st32(tO + c * 32, o);
+              }
+              tmem_st_wait();
+              l *= g;
+              m_use = m_new;
+            } else if (m_use == -INFINITY) {
+              m_use = m_new;
+            }
+            const float nb = m_use == -INFINITY ? 0.f : -m_use;
+            const float2 sl2v = make_float2(sl2, sl2), nbv = make_float2(nb, nb);
+            float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            auto emit = [&](const uint32_t (&v)[64], int hf) {
+              uint32_t pb[32];
+#pragma unroll
+              for (int j = 0; j < 64; j += 2) {
+                const float2 t2 = __ffma2_rn(
+                    make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sl2v, nbv);
+                const float2 e = make_float2(ex2(t2.x), ex2(t2.y));
+                s2[(j >> 1) & 1] = __fadd2_rn(s2[(j >> 1) & 1], e);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(e.x, e.y);
+                pb[j >> 1] = *reinterpret_cast<const uint32_t *>(&b);
+              }
+              tmem_st32(tS + hf * 32, pb);
+            };
+            emit(sa, 0);
+            emit(sb, 1);
+            l += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
+            tmem_st_wait();
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[x]);
+        }
+        if (!ok) break;
+        // ---- the piece's result
+        if (!__all_sync(FULL, mbar_wait(&pv_done[x], (ns - 1) & 1))) {
           p_fail(io.status, abort_flag);
           ok = false;
           break;
         }
         fence_after();
         if (warp_on) {
-          const int lim = seen - t * PAGED_TC_KT;
-          // the row of S: two 64-column loads
-          uint32_t sa[64], sb[64];
-          tmem_ld64(tS, sa);
-          tmem_ld64(tS + 64, sb);
-          tmem_ld_wait64(sa);
-          tmem_ld_wait64(sb);
-          if (__any_sync(FULL, lim < PAGED_TC_KT)) {
-#pragma unroll
-            for (int j = 0; j < 64; ++j) {
-              if (j >= lim) sa[j] = __float_as_uint(-INFINITY);
-              if (64 + j >= lim) sb[j] = __float_as_uint(-INFINITY);
-            }
-          }
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto fold_max = [&](const uint32_t (&v)[64]) {
-#pragma unroll
-            for (int j = 0; j < 64; j += 2)
-              m4[(j >> 1) & 3] = max3(m4[(j >> 1) & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+          const int worker = paged_first_worker(io, kind) +
+                             (kind == PAGED_WIDE ? (int)blockIdx.x : 2 * (int)blockIdx.x + x);
+          const PagedDest dest = paged_dest(p, io, w, worker);
+          const int on = min(32, rows - q4 * 32);       // rows of this warp
+          const bool out = dest.kind == PAGED_OUT;
+          // Rows leave through shared memory, so that 8 lanes write 32 columns of one row together:
+          // stored straight from the lanes that hold them, each store touched 32 lines (9000 cycles
+          // for 256 rows of 128 fp32 columns).
+          const int tok_w = w.s.tok0 + w.tok + tile0, h0 = w.head * rep;
+          auto dst_row = [&](int i) {   // of row i of this warp
+            const int rr = q4 * 32 + i;
+            return paged_dest_row(io, dest, tile0 * rep + rr, tok_w + rr / rep, h0 + rr % rep);
           };
-          fold_max(sa);
-          fold_max(sb);
-          const float m_new = fmaxf(m_use, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2);
-          // O is rescaled only when a row's maximum grew by more than 2^8 (P stays below 256, and O
-          // and l share their base, so O / l does not change); S of this tile was issued behind the
-          // last P V, so O includes it
-          if (__any_sync(FULL, m_use != -INFINITY && m_new > m_use + P_RESCALE)) {
-            const float f = m_use == -INFINITY ? 1.f : ex2(m_use - m_new);
+          const size_t base = paged_dest_base(p, io, dest);
+          int row8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) row8[i] = dst_row(i * 4 + (lane >> 3));
+          const float g = out ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
 #pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tO + c * 32, o);
-              tmem_ld_wait(o);
+          for (int c = 0; c < HD / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_ld_wait(o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st32(tO + c * 32, o);
+            for (int j = 0; j < 8; ++j)
+              stage[lane * 8 + (j ^ (lane & 7))] =
+                  make_float4(__uint_as_float(o[4 * j]) * g, __uint_as_float(o[4 * j + 1]) * g,
+                              __uint_as_float(o[4 * j + 2]) * g, __uint_as_float(o[4 * j + 3]) * g);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int rr = i * 4 + (lane >> 3), col = c * 32 + (lane & 7) * 4;
+              if (i * 4 >= on) break;
+              const float4 v = stage[rr * 8 + ((lane & 7) ^ (rr & 7))];
+              if (rr < on) {
+                const size_t e = (base + row8[i]) * HD + col;
+                if (out) store4<bf16>((bf16 *)io.out + e, v.x, v.y, v.z, v.w);
+                else *reinterpret_cast<float4 *>(io.part_o + e) = v;
+              }
             }
-            tmem_st_wait();
-            l *= f;
-            m_use = m_new;
-          } else if (m_use == -INFINITY) {
-            m_use = m_new;
+            __syncwarp();
           }
-          const float nb = m_use == -INFINITY ? 0.f : -m_use;
-          const float2 sl2v = make_float2(sl2, sl2), nbv = make_float2(nb, nb);
-          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          auto emit = [&](const uint32_t (&v)[64], int hf) {
-            uint32_t pb[32];
-#pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-              const float2 t2 = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
-                                           sl2v, nbv);
-              const float2 e = make_float2(ex2(t2.x), ex2(t2.y));
-              s2[(j >> 1) & 1] = __fadd2_rn(s2[(j >> 1) & 1], e);
-              const __nv_bfloat162 b = __floats2bfloat162_rn(e.x, e.y);
-              pb[j >> 1] = *reinterpret_cast<const uint32_t *>(&b);
-            }
-            tmem_st32(tS + hf * 32, pb);
-          };
-          emit(sa, 0);
-          emit(sb, 1);
-          l += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
-          tmem_st_wait();
+          if (!out && lane < on) {
+            io.part_ml[base + dst_row(lane)] = make_float2(m_use, l);
+            if (dest.redirect) paged_redirect(p, io, dest, worker, tok_w + r / rep, h0 + r % rep);
+          }
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (lane == 0) mbar_arrive(&o_empty[x]);
       }
-      if (!ok) break;
-      // ---- the piece's result
-      const int chain_tiles = pc.narrow ? (pc.t1 - pc.t0 + 1 - x) / 2 : pc.t1 - pc.t0;
-      if (chain_tiles > 0 && !__all_sync(FULL, mbar_wait(&pv_done[x], (ns - 1) & 1))) {
-        p_fail(io.status, abort_flag);
-        break;
-      }
-      fence_after();
-      float fa = 1.f, fb = 0.f;   // factors of the two chains' O
-      if (pc.narrow) {
-        if (x == 1) {
-          // chain A stores for both; it is done with the (m, l) handed over before when it has freed
-          // the accumulators of the previous piece
-          if (pieces > 0 && !__all_sync(FULL, mbar_wait(&o_empty[1], (pieces - 1) & 1))) {
-            p_fail(io.status, abort_flag);
-            break;
+    }
+    // ---- few-row items
+    // this warp has left its chain; when all eight have, the rings and query tiles are idle
+    __syncwarp();
+    if (lane == 0) mbar_arrive(chains_done);
+    if (ok && few_start.u0 < few_start.u1) {
+      constexpr int SLOT = F_KT * HD * 2;                       // 16 keys: [half][16 rows][128 bytes]
+      const int fw = warp - 4, gr = lane >> 2, tq = lane & 3;   // fragment row and column pair
+      uint8_t *ring = sQ + fw * F_SLOTS * SLOT;
+      uint64_t *bar = f_full + fw * F_SLOTS;
+      uint32_t issued = 0, taken = 0;                           // slots (K and V of a step in turn)
+      ok = __all_sync(FULL, mbar_wait(chains_done, 0));
+      // copies run F_SLOTS / 2 steps ahead of the arithmetic, across items; page ids one step further
+      PagedWalk lw;
+      int lt = 0, ly = 0;
+      auto lookup = [&]() {
+        const long long row = paged_row(io, p, lw.s.seq, lw.head, lw.s.key0 + lt * F_KT);
+        ly = row < 0 ? (io.n_pages * p.Hkv) << io.page_shift : (int)row;   // past the pool: zeros
+      };
+      auto issue = [&]() {
+        if (!lw.more()) return;
+        if (lane == 0) {
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t s = (issued + kv) % F_SLOTS;
+            mbar_expect_tx(&bar[s], SLOT);
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h)
+              tma_load_2d(ring + s * SLOT + h * (F_KT * 128), kv ? &tmVf : &tmKf, &bar[s], h * 64, ly);
           }
-          b_ml[r] = make_float2(m_use, l);
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_done);
-          continue;
         }
-        if (!__all_sync(FULL, mbar_wait(b_done, narrows & 1))) {
-          p_fail(io.status, abort_flag);
-          break;
+        issued += 2;
+        if (++lt == lw.t1) {
+          lw.next(p);
+          lt = lw.t0;
         }
-        ++narrows;
-        fence_after();
-        if (pc.t1 - pc.t0 > 1) {
-          const float2 mb = b_ml[r];
-          const float m = fmaxf(m_use, mb.x), base = m == -INFINITY ? 0.f : m;
-          fa = ex2(m_use - base);
-          fb = ex2(mb.x - base);
-          l = l * fa + mb.y * fb;
-          m_use = m;
-        }
+        if (lw.more()) lookup();
+      };
+      lw.begin(p, PAGED_FEW, few_start);
+      if (ok && lw.more()) {
+        lt = lw.t0;
+        lookup();
+        for (int i = 0; i < F_SLOTS / 2; ++i) issue();
       }
-      if (warp_on) {
-        const bool both = pc.narrow && pc.t1 - pc.t0 > 1;   // O_B holds something
-        const PagedDest dest = paged_dest(p, io, w, blockIdx.x);
-        const int tok = w.s.tok0 + pc.i0 + tl, h = w.head * rep + r % rep;
-        const float il = l > 0.f ? 1.f / l : 0.f;
-        bf16 *out = (bf16 *)io.out + ((size_t)tok * io.Hq + h) * HD;
-        const size_t prow = paged_part_row(p, io, dest, tile0 * rep + r, tok, h);
-        float *part = io.part_o + prow * HD;
-#pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + c * 32, o);
-          tmem_ld_wait(o);
-          if (both) {
-            uint32_t ob[32];
-            tmem_ld32(tO + 128 + c * 32, ob);
-            tmem_ld_wait(ob);
+      PagedWalk w;
+      for (w.begin(p, PAGED_FEW, few_start); ok && w.more(); w.next(p)) {
+        const int rows = w.toks * rep, h0 = w.head * rep, tok_w = w.s.tok0 + w.tok;
+        uint32_t qf[HD / 16][4];   // Q as the A operand: rows gr and gr + 8
+        const bf16 *q0 = (const bf16 *)io.q + ((size_t)(tok_w + gr / rep) * io.Hq + h0 + gr % rep) * HD;
+        const bf16 *q1 = (const bf16 *)io.q +
+                         ((size_t)(tok_w + (gr + 8) / rep) * io.Hq + h0 + (gr + 8) % rep) * HD;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              o[j] = __float_as_uint(__uint_as_float(o[j]) * fa + __uint_as_float(ob[j]) * fb);
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const int c = kk * 16 + tq * 2;
+          qf[kk][0] = gr < rows ? *reinterpret_cast<const uint32_t *>(q0 + c) : 0u;
+          qf[kk][1] = gr + 8 < rows ? *reinterpret_cast<const uint32_t *>(q1 + c) : 0u;
+          qf[kk][2] = gr < rows ? *reinterpret_cast<const uint32_t *>(q0 + c + 8) : 0u;
+          qf[kk][3] = gr + 8 < rows ? *reinterpret_cast<const uint32_t *>(q1 + c + 8) : 0u;
+        }
+        int seen[2];               // keys that rows gr and gr + 8 see
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          seen[i] = w.s.causal ? w.s.keys - w.s.n + w.tok + min(gr + 8 * i, rows - 1) / rep + 1 : w.keys;
+        float o[HD / 8][4], m[2] = {-INFINITY, -INFINITY}, ls[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < HD / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        for (int t = w.t0; t < w.t1; ++t, taken += 2) {
+          const int k0 = t * F_KT, live = min(F_KT, w.keys - k0);
+          const uint32_t ks = taken % F_SLOTS, vs = (taken + 1) % F_SLOTS;
+          if (!__all_sync(FULL, mbar_wait(&bar[ks], (taken / F_SLOTS) & 1))) { ok = false; break; }
+          float s[2][4] = {};
+          const uint8_t *K = ring + ks * SLOT;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            uint32_t b[4];
+            const int mi = lane >> 3, key = (mi >> 1) * 8 + (lane & 7);
+            const int chunk = (kk & 3) * 2 + (mi & 1);        // of the 8 chunks of a 128-byte row
+            ldsm_x4(b, K + (kk >> 2) * (F_KT * 128) + key * 128 + ((chunk ^ (key & 7)) << 4));
+            mma_16816(s[0], qf[kk], b[0], b[1]);
+            mma_16816(s[1], qf[kk], b[2], b[3]);
           }
-          if (!row_ok) continue;   // guards the stores only; every lane reads tensor memory
-          if (dest.kind == PAGED_OUT) {
+          // rows gr (i = 0) and gr + 8: mask, running maximum, numerators
+          float mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint32_t v[4];
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(
-                    __uint_as_float(o[j + 2 * e]) * il, __uint_as_float(o[j + 2 * e + 1]) * il);
-                v[e] = *reinterpret_cast<const uint32_t *>(&b2);
-              }
-              *reinterpret_cast<uint4 *>(out + c * 32 + j) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int e = 0; e < 4; ++e) {
+              const int key = k0 + j * 8 + tq * 2 + (e & 1);
+              s[j][e] = key < seen[e >> 1] ? s[j][e] * sl2 : -INFINITY;
+              mt[e >> 1] = fmaxf(mt[e >> 1], s[j][e]);
             }
-          } else {
+          float grow = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4 *>(part + c * 32 + j) =
-                  make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          for (int i = 0; i < 2; ++i) {
+            mt[i] = fmaxf(mt[i], __shfl_xor_sync(FULL, mt[i], 1));
+            mt[i] = fmaxf(mt[i], __shfl_xor_sync(FULL, mt[i], 2));
+            if (m[i] == -INFINITY) m[i] = mt[i];
+            else grow = fmaxf(grow, mt[i] - m[i]);
+          }
+          if (__any_sync(FULL, grow > P_RESCALE)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float mn = fmaxf(m[i], mt[i]);
+              const float g = m[i] == -INFINITY ? 1.f : ex2(m[i] - mn);
+              m[i] = mn;
+              ls[i] *= g;
+#pragma unroll
+              for (int j = 0; j < HD / 8; ++j) {
+                o[j][2 * i] *= g;
+                o[j][2 * i + 1] *= g;
+              }
+            }
+          }
+          // P as the A operand in two bf16 parts (16 significant bits; these products are cheap)
+          uint32_t ph[4], pl[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float base = m[i] == -INFINITY ? 0.f : m[i];
+              const float e0 = ex2(s[j][2 * i] - base), e1 = ex2(s[j][2 * i + 1] - base);
+              ls[i] += e0 + e1;
+              const __nv_bfloat162 hi = __floats2bfloat162_rn(e0, e1);
+              const __nv_bfloat162 lo =
+                  __floats2bfloat162_rn(e0 - __low2float(hi), e1 - __high2float(hi));
+              ph[2 * j + i] = *reinterpret_cast<const uint32_t *>(&hi);
+              pl[2 * j + i] = *reinterpret_cast<const uint32_t *>(&lo);
+            }
+          if (!__all_sync(FULL, mbar_wait(&bar[vs], ((taken + 1) / F_SLOTS) & 1))) { ok = false; break; }
+          uint8_t *V = ring + vs * SLOT;
+          if (live < F_KT) {   // rows past the last key: zeros, whatever they hold
+            for (int e = lane; e < (F_KT - live) * 8; e += 32)
+#pragma unroll
+              for (int h = 0; h < HALVES; ++h)
+                reinterpret_cast<uint4 *>(V + h * (F_KT * 128) + live * 128)[e] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();   // before the copy that overwrites them later
+            __syncwarp();
+          }
+#pragma unroll
+          for (int nn = 0; nn < HD / 16; ++nn) {
+            uint32_t b[4];
+            const int mi = lane >> 3, key = (mi & 1) * 8 + (lane & 7);
+            const int chunk = (nn & 3) * 2 + (mi >> 1);
+            ldsm_x4_t(b, V + (nn >> 2) * (F_KT * 128) + key * 128 + ((chunk ^ (key & 7)) << 4));
+            mma_16816(o[2 * nn], ph, b[0], b[1]);
+            mma_16816(o[2 * nn], pl, b[0], b[1]);
+            mma_16816(o[2 * nn + 1], ph, b[2], b[3]);
+            mma_16816(o[2 * nn + 1], pl, b[2], b[3]);
+          }
+          __syncwarp();   // every lane has read the step's slots
+          issue();
+        }
+        if (!ok) break;
+        const int worker = paged_first_worker(io, PAGED_FEW) + 8 * blockIdx.x + fw;
+        const PagedDest dest = paged_dest(p, io, w, worker);
+        const size_t base = paged_dest_base(p, io, dest);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ls[i] += __shfl_xor_sync(FULL, ls[i], 1);
+          ls[i] += __shfl_xor_sync(FULL, ls[i], 2);
+          const int rr = gr + 8 * i;
+          if (rr >= rows) continue;
+          const int tok = tok_w + rr / rep, h = h0 + rr % rep;
+          const size_t row = base + paged_dest_row(io, dest, rr, tok, h);
+          if (dest.kind == PAGED_OUT) {
+            const float il = ls[i] > 0.f ? 1.f / ls[i] : 0.f;
+            bf16 *dst = (bf16 *)io.out + row * HD + tq * 2;
+#pragma unroll
+            for (int j = 0; j < HD / 8; ++j)
+              *reinterpret_cast<__nv_bfloat162 *>(dst + j * 8) =
+                  __floats2bfloat162_rn(o[j][2 * i] * il, o[j][2 * i + 1] * il);
+          } else {
+            float *dst = io.part_o + row * HD + tq * 2;
+#pragma unroll
+            for (int j = 0; j < HD / 8; ++j)
+              *reinterpret_cast<float2 *>(dst + j * 8) = make_float2(o[j][2 * i], o[j][2 * i + 1]);
+            if (tq == 0) {
+              io.part_ml[row] = make_float2(m[i], ls[i]);
+              if (dest.redirect) paged_redirect(p, io, dest, worker, tok, h);
+            }
           }
         }
-        if (row_ok && dest.kind != PAGED_OUT) {
-          io.part_ml[prow] = make_float2(m_use, l);
-          if (dest.redirect) paged_redirect(p, io, dest, blockIdx.x, tok, h);
-        }
       }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&o_empty[x]);
-        if (pc.narrow) mbar_arrive(&o_empty[1]);
+      if (!ok) {
+        if (lane == 0) p_fail(io.status, abort_flag);
+        for (uint32_t i = taken; i < issued; ++i)   // what is still in flight lands
+          (void)mbar_wait(&bar[i % F_SLOTS], (i / F_SLOTS) & 1);
       }
     }
   }
@@ -560,18 +797,22 @@ int run_tc(const PagedCall &c, const PagedShape &p, const PagedIO &io, cudaStrea
     return cudaFuncGetAttributes(&fa, paged_attn_tc_kernel<HD>) == cudaSuccess ? fa.numRegs : -1;
   }();
   if (regs < P_REGS) return DG_ERR_UNSUPPORTED;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, tkf, tvf;
   const uint64_t rows = (uint64_t)c.n_pages * c.Hkv * c.page_size;
   const uint32_t box = c.page_size < PAGED_TC_KT ? c.page_size : PAGED_TC_KT;
   const CUtensorMapDataType bt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  int rc = make_tmap_3d(&tq, bt, 2, c.q, HD, c.Hq, c.n_tokens, 64, io.rep, p.qn);
+  int rc = make_tmap_3d(&tq, bt, 2, c.q, HD, c.Hq, c.n_tokens, HD * 2,
+                        (uint64_t)c.Hq * HD * 2, 64, io.rep, p.qn);
   if (rc == DG_OK) rc = make_tmap_2d(&tk, bt, 2, c.k_pages, HD, rows, HD * 2, 64, box);
   if (rc == DG_OK) rc = make_tmap_2d(&tv, bt, 2, c.v_pages, HD, rows, HD * 2, 64, box);
+  if (rc == DG_OK) rc = make_tmap_2d(&tkf, bt, 2, c.k_pages, HD, rows, HD * 2, 64, F_KT);
+  if (rc == DG_OK) rc = make_tmap_2d(&tvf, bt, 2, c.v_pages, HD, rows, HD * 2, 64, F_KT);
   if (rc != DG_OK) return rc;
   note_launch(s, "paged_attn_tc");
   cudaFuncSetAttribute(paged_attn_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)C::SMEM);
-  launch_pdl(paged_attn_tc_kernel<HD>, io.ctas, P_THR, C::SMEM, s, tq, tk, tv, p, io);
+  launch_pdl(paged_attn_tc_kernel<HD>, io.ctas, P_THR, C::SMEM, s, tq, tk, tv, tkf, tvf, p,
+             io);
   return check_launch("paged_attn_tc");
 }
 

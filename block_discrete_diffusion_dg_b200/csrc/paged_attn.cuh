@@ -14,10 +14,13 @@ struct PagedIO {
   const int32_t *page_table;     // [n_seqs][max_pages]
   int n_pages, max_pages, page_shift;
   int Hq, rep;
-  int rows;                      // rows of a partial result's slot
   int ctas;
-  PagedHead *heads;              // [ctas]
-  // rows of fp32 partial results: 2 slots per CTA, then (shared prefix) a region [2][n_tokens][Hq]
+  int workers;                   // of all kinds (see paged_worker)
+  int rows[3];                   // rows of a partial result's slot, by kind of item
+  PagedHead *heads;              // [workers]
+  // rows of fp32 partial results: 2 slots per worker, then (shared prefix) a region
+  // [2][n_tokens][Hq]
+  size_t region;                 // its first row
   float *part_o;
   float2 *part_ml;               // (m, l) of each row; l < 0 in the region: see paged_redirect
   int32_t *status;
@@ -25,6 +28,10 @@ struct PagedIO {
 
 // Tensor-core kernel (k_paged_attn_tc.cu): query rows and keys per tile.
 constexpr int PAGED_TC_ROWS = 128, PAGED_TC_KT = 128;
+constexpr int PAGED_TC_FEW = 16, PAGED_TC_FEW_KT = 16;   // of few-row items: rows at most, keys per step
+// Starting and storing an item, in key tiles of its kind.
+constexpr int PAGED_TC_START_WIDE = 2, PAGED_TC_START_NARROW = 1, PAGED_TC_START_FEW = 4;
+constexpr int PAGED_TC_LEAST_FEW = 4;
 inline bool paged_tc_supported(int act, int hd) { return act == DG_BF16 && (hd == 64 || hd == 128); }
 struct PagedCall;
 int launch_paged_tc(const PagedCall &c, const PagedShape &p, const PagedIO &io, cudaStream_t s);
@@ -46,6 +53,14 @@ __device__ __forceinline__ void paged_report(const PagedIO &io, int error) {
 }
 
 // ---- destinations -------------------------------------------------------------------------------
+// Workers are numbered through: wide ones [0, ctas), narrow ones (two per CTA) [ctas, 3 ctas), few-row
+// ones (eight per CTA) [3 ctas, 11 ctas).
+__host__ __device__ inline int paged_first_worker(const PagedIO &io, int kind) {
+  return kind == PAGED_WIDE ? 0 : kind == PAGED_NARROW ? io.ctas : 3 * io.ctas;
+}
+__host__ __device__ inline int paged_worker_kind(const PagedIO &io, int worker) {
+  return worker < io.ctas ? PAGED_WIDE : worker < 3 * io.ctas ? PAGED_NARROW : PAGED_FEW;
+}
 enum { PAGED_OUT = 0, PAGED_REGION = 1, PAGED_SLOT = 2 };
 struct PagedDest {
   int kind;
@@ -54,51 +69,50 @@ struct PagedDest {
   bool redirect;  // the first of several pieces: the region entry points to them
 };
 
-__device__ __forceinline__ size_t paged_slot_row(const PagedIO &io, int cta, bool begins, int r) {
-  return (size_t)(2 * cta + (begins ? 1 : 0)) * io.rows + r;
+// Slots lie kind by kind; paged_slot_row(io, io.workers, false, 0) is their total.
+__host__ __device__ inline size_t paged_slot_row(const PagedIO &io, int worker, bool begins, int r) {
+  const int kind = paged_worker_kind(io, worker);
+  size_t base = 0;
+  if (kind >= PAGED_NARROW) base += (size_t)2 * io.ctas * io.rows[PAGED_WIDE];
+  if (kind == PAGED_FEW) base += (size_t)4 * io.ctas * io.rows[PAGED_NARROW];
+  return base +
+         (size_t)(2 * (worker - paged_first_worker(io, kind)) + (begins ? 1 : 0)) * io.rows[kind] + r;
 }
 __device__ __forceinline__ size_t paged_region_row(const PagedShape &p, const PagedIO &io,
                                                    int which, int tok, int h) {
-  return (size_t)2 * io.ctas * io.rows + ((size_t)which * p.n_tokens + tok) * io.Hq + h;
+  return io.region + ((size_t)which * p.n_tokens + tok) * io.Hq + h;
 }
 
 // Where the current piece of a walk goes: a whole item to the output (or its half of the region),
-// a part of one to a slot of this CTA (slot 1 if the item begins here, slot 0 if it goes on from
-// an earlier CTA; a range holds at most one of each).
+// a part of one to a slot of this worker (slot 1 if the item begins here, slot 0 if it goes on from
+// an earlier worker; a range holds at most one of each).
 __device__ __forceinline__ PagedDest paged_dest(const PagedShape &p, const PagedIO &io,
-                                                const PagedWalk &w, int cta) {
+                                                const PagedWalk &w, int worker) {
   PagedDest d;
   d.which = p.shared_len > 0 && w.seg == 0 ? 0 : 1;
-  const bool begins = w.k0() == 0;
-  const bool whole = begins && w.k1() == w.units();
-  d.kind = !whole ? PAGED_SLOT : p.shared_len > 0 ? PAGED_REGION : PAGED_OUT;
-  d.slot = paged_slot_row(io, cta, begins, 0);
-  d.redirect = d.kind == PAGED_SLOT && begins && p.shared_len > 0;
+  d.kind = !w.whole() ? PAGED_SLOT : p.shared_len > 0 ? PAGED_REGION : PAGED_OUT;
+  d.slot = paged_slot_row(io, worker, w.t0 == 0, 0);
+  d.redirect = d.kind == PAGED_SLOT && w.t0 == 0 && p.shared_len > 0;
   return d;
+}
+// Row of the destination that holds packed row (tok, h), row r of the item, without the base.
+__device__ __forceinline__ size_t paged_dest_base(const PagedShape &p, const PagedIO &io,
+                                                  const PagedDest &d) {
+  return d.kind == PAGED_SLOT     ? d.slot
+         : d.kind == PAGED_REGION ? paged_region_row(p, io, d.which, 0, 0)
+                                  : 0;
+}
+__device__ __forceinline__ int paged_dest_row(const PagedIO &io, const PagedDest &d, int r, int tok,
+                                              int h) {
+  return d.kind == PAGED_SLOT ? r : tok * io.Hq + h;
 }
 __device__ __forceinline__ size_t paged_part_row(const PagedShape &p, const PagedIO &io,
                                                  const PagedDest &d, int r, int tok, int h) {
   return d.kind == PAGED_SLOT ? d.slot + r : paged_region_row(p, io, d.which, tok, h);
 }
 __device__ __forceinline__ void paged_redirect(const PagedShape &p, const PagedIO &io,
-                                               const PagedDest &d, int cta, int tok, int h) {
-  io.part_ml[paged_region_row(p, io, d.which, tok, h)] = make_float2(__int_as_float(cta), -1.f);
-}
-
-// The item that the range of CTA `cta` begins inside, for the join kernels.
-__device__ __forceinline__ void paged_write_head(const PagedShape &p, const PagedIO &io,
-                                                 const PagedStart &st, int cta) {
-  PagedHead h{};
-  if (st.u0 < st.u1 && st.u0 > st.item_u0) {
-    const PagedSeg s = paged_seg(p, st.seg);
-    const long long end = st.item_u0 + paged_item_units(p, s, st.item);
-    h.joins = st.u0 - st.item_u0 <= st.per;
-    h.last = (int)((end - 1) / st.per);
-    h.tok0 = s.tok0 + st.item * p.qt;
-    h.tokens = paged_item_tokens(p, s, st.item);
-    h.head = st.head;
-  }
-  io.heads[cta] = h;
+                                               const PagedDest &d, int worker, int tok, int h) {
+  io.part_ml[paged_region_row(p, io, d.which, tok, h)] = make_float2(__int_as_float(worker), -1.f);
 }
 
 }  // namespace dg

@@ -1,12 +1,17 @@
 // How the paged attention splits its work over a fixed grid.
 //
-// Every query tile of a sequence (an "item": the query heads of one kv head times up to `qt`
-// consecutive tokens) costs one unit per key tile it visits.  All units of the call, ordered by
-// (sequence, kv head, item, key tile), are cut into equal ranges of `per` units, one per CTA, so
-// the load is even whatever the lengths are: a batch of short and long sequences, the triangle of
-// a causal prompt, or one long context with a few rows.  An item cut by a range boundary leaves
-// one partial result per piece, and the pieces are joined afterwards in the order of their keys.
-// Lengths live on the device, so each CTA derives its range itself: a warp scans the sequences
+// An item is the query heads of one kv head times up to `qt` consecutive tokens of a sequence, against
+// the key tiles they see; its cost is the number of those tiles plus a constant for starting and
+// storing it.  The costs of all items, ordered by (sequence, kv head, item, key tile), are cut into
+// equal ranges, one per worker, so the load is even whatever the lengths are: a batch of short and
+// long sequences, the triangle of a causal prompt, or one long context with a few rows.  An item cut
+// by a range boundary leaves one partial result per piece, and the pieces are joined afterwards in the
+// order of their keys.
+// There are three kinds of items, each with workers of its own: wide items (two query tiles that share
+// each key tile; a worker is a CTA), narrow ones (a sequence's last item if it has at most `qn` tokens:
+// one query tile; a worker is one of a CTA's two chains) and few-row ones (the last item if it has at
+// most `qf` tokens: single tokens and short tails; a worker is one of eight warps of a CTA).
+// Lengths live on the device, so each worker derives its range itself: a warp scans the sequences
 // (32 at a time) and searches the item within the sequence.
 #pragma once
 
@@ -26,8 +31,12 @@ struct PagedShape {
   int n_seqs, n_tokens;     // n_tokens: packed rows of q and out
   int Hkv;
   int qt;                   // tokens per item
-  int qn;                   // an item of at most qn tokens is narrow: one unit covers two key tiles
-  int kt;                   // keys per tile
+  int qn;                   // a last item of at most qn tokens is narrow (0: none is),
+  int qf;                   // of at most qf <= qn few-row (0: none is)
+  // by kind of item:
+  int kt[3];                // keys per tile
+  int start_cost[3];        // cost of starting and storing an item, in key tiles
+  int least[3];             // least cost worth a worker of its own
   int causal;
   int shared_len;           // > 0: keys [0, shared_len) form segment 0, seen by every token
   int cap;                  // keys a page-table row can address
@@ -105,7 +114,22 @@ DG_HD long long floor_sum(long long n, long long m, long long a, long long b) {
   return r;
 }
 
-DG_HD int paged_items(const PagedShape &p, const PagedSeg &s) { return (s.n + p.qt - 1) / p.qt; }
+enum { PAGED_WIDE = 0, PAGED_NARROW = 1, PAGED_FEW = 2 };
+
+// The kind of a segment's last item where it is not wide, else PAGED_WIDE.
+DG_HD int paged_tail_kind(const PagedShape &p, const PagedSeg &s) {
+  const int tail = s.n % p.qt;
+  return tail == 0 || tail > p.qn ? PAGED_WIDE : tail > p.qf ? PAGED_NARROW : PAGED_FEW;
+}
+// Items of a kind in one kv head of segment s, and the index of the first.
+DG_HD int paged_items(const PagedShape &p, const PagedSeg &s, int kind) {
+  const int tail = paged_tail_kind(p, s);
+  if (kind != PAGED_WIDE) return tail == kind ? 1 : 0;
+  return tail == PAGED_WIDE ? (s.n + p.qt - 1) / p.qt : s.n / p.qt;
+}
+DG_HD int paged_first_item(const PagedShape &p, const PagedSeg &s, int kind) {
+  return kind == PAGED_WIDE ? 0 : s.n / p.qt;
+}
 DG_HD int paged_item_tokens(const PagedShape &p, const PagedSeg &s, int i) {
   const int left = s.n - i * p.qt;
   return left < p.qt ? left : p.qt;
@@ -115,41 +139,41 @@ DG_HD int paged_item_keys(const PagedShape &p, const PagedSeg &s, int i) {
   if (!s.causal) return s.keys;
   return s.keys - s.n + i * p.qt + paged_item_tokens(p, s, i);
 }
-DG_HD int paged_item_tiles(const PagedShape &p, const PagedSeg &s, int i) {
-  return (paged_item_keys(p, s, i) + p.kt - 1) / p.kt;
+DG_HD int paged_item_tiles(const PagedShape &p, const PagedSeg &s, int kind, int i) {
+  return (paged_item_keys(p, s, i) + p.kt[kind] - 1) / p.kt[kind];
 }
-DG_HD int paged_item_units(const PagedShape &p, const PagedSeg &s, int i) {
-  const int t = paged_item_tiles(p, s, i);
-  return paged_item_tokens(p, s, i) <= p.qn ? (t + 1) / 2 : t;
+// Cost of the first q items of a kind (of one kv head).
+DG_HD long long paged_cost_before(const PagedShape &p, const PagedSeg &s, int kind, int q) {
+  if (q <= 0) return 0;
+  if (kind != PAGED_WIDE)
+    return paged_item_tiles(p, s, kind, paged_first_item(p, s, kind)) + p.start_cost[kind];
+  const long long start = (long long)q * p.start_cost[kind];
+  if (!s.causal) return start + (long long)q * paged_item_tiles(p, s, kind, 0);
+  // full items by their sum, the last one (which may have fewer tokens) by itself
+  const bool last = q == paged_items(p, s, kind);
+  const long long r =
+      floor_sum(last ? q - 1 : q, p.kt[kind], p.qt,
+                (long long)s.keys - s.n + p.qt + p.kt[kind] - 1);
+  return start + (last ? r + paged_item_tiles(p, s, kind, q - 1) : r);
 }
-// Units of the first q items (of one kv head); every item but the last is full and wide.
-DG_HD long long paged_units_before(const PagedShape &p, const PagedSeg &s, int q) {
-  const int items = paged_items(p, s);
-  if (q <= 0 || items == 0) return 0;
-  const int wide = q < items ? q : items - 1;
-  long long r;
-  if (s.causal)
-    r = floor_sum(wide, p.kt, p.qt, (long long)s.keys - s.n + p.qt + p.kt - 1);
-  else
-    r = (long long)wide * ((s.keys + p.kt - 1) / p.kt);
-  return q < items ? r : r + paged_item_units(p, s, items - 1);
-}
-DG_HD long long paged_seg_units(const PagedShape &p, const PagedSeg &s) {
-  return s.n > 0 ? p.Hkv * paged_units_before(p, s, paged_items(p, s)) : 0;
+DG_HD long long paged_head_cost(const PagedShape &p, const PagedSeg &s, int kind) {
+  return s.n > 0 ? paged_cost_before(p, s, kind, paged_items(p, s, kind)) : 0;
 }
 
-// One CTA's place in the work: the item it begins in and the unit range it owns.
+// A worker's place in the work of a kind: its range [u0, u1) of the total cost (u0 >= u1: none) and
+// the item that it begins in.
 struct PagedStart {
-  long long u0, u1;         // owned units [u0, u1); u0 >= u1: none
-  long long item_u0;        // first unit of the item that holds u0
-  long long per;            // units per CTA
+  long long u0, u1;
+  long long item_u0;        // where the item that holds u0 begins
+  long long per;            // cost per worker
   int seg, head, item;
 };
 
 #ifdef __CUDACC__
 // Called by one whole warp.  *error: the largest error code of any sequence, for the caller to
 // record.
-__device__ inline PagedStart paged_locate(const PagedShape &p, int cta, int ctas, int *error) {
+__device__ inline PagedStart paged_locate(const PagedShape &p, int kind, int worker, int workers,
+                                          int *error) {
   const int lane = threadIdx.x & 31;
   const unsigned full = 0xffffffffu;
   const int segs = paged_segs(p);
@@ -159,7 +183,7 @@ __device__ inline PagedStart paged_locate(const PagedShape &p, int cta, int ctas
     long long w = 0;
     if (b + lane < segs) {
       const PagedSeg s = paged_seg(p, b + lane);
-      w = paged_seg_units(p, s);
+      w = p.Hkv * paged_head_cost(p, s, kind);
       err = err > s.error ? err : s.error;
     }
 #pragma unroll
@@ -173,8 +197,9 @@ __device__ inline PagedStart paged_locate(const PagedShape &p, int cta, int ctas
   }
   *error = err;
   PagedStart r;
-  r.per = (total + ctas - 1) / ctas;
-  r.u0 = cta * r.per;
+  r.per = (total + workers - 1) / workers;
+  if (r.per < p.least[kind]) r.per = p.least[kind];
+  r.u0 = worker * r.per;
   r.u1 = r.u0 + r.per < total ? r.u0 + r.per : total;
   r.seg = r.head = r.item = 0;
   r.item_u0 = 0;
@@ -185,7 +210,7 @@ __device__ inline PagedStart paged_locate(const PagedShape &p, int cta, int ctas
   long long before = 0;
   for (int b = 0; b < segs; b += 32) {
     long long w = 0;
-    if (b + lane < segs) w = paged_seg_units(p, paged_seg(p, b + lane));
+    if (b + lane < segs) w = p.Hkv * paged_head_cost(p, paged_seg(p, b + lane), kind);
     long long inc = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -202,71 +227,104 @@ __device__ inline PagedStart paged_locate(const PagedShape &p, int cta, int ctas
     before += __shfl_sync(full, inc, 31);
   }
   const PagedSeg s = paged_seg(p, r.seg);
-  const long long each = paged_units_before(p, s, paged_items(p, s));
+  const long long each = paged_head_cost(p, s, kind);
   r.head = (int)((r.u0 - before) / each);
   before += r.head * each;
-  // the last item whose first unit is <= u0: 32-way search
-  int lo = 0, hi = paged_items(p, s);
+  // the last item that begins at or before u0: 32-way search
+  int lo = 0, hi = paged_items(p, s, kind);
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-    const bool le = i < hi && before + paged_units_before(p, s, i) <= r.u0;
+    const bool le = i < hi && before + paged_cost_before(p, s, kind, i) <= r.u0;
     const int l = 31 - __clz(__ballot_sync(full, le));  // lane 0 always holds
     lo += l * step;
     hi = hi < lo + step ? hi : lo + step;
   }
   r.item = lo;
-  r.item_u0 = before + paged_units_before(p, s, lo);
+  r.item_u0 = before + paged_cost_before(p, s, kind, lo);
   return r;
 }
 #endif
 
-// Walks the pieces of a CTA's range [u0, u1) in order: after begin(), while (more()), units
-// [k0(), k1()) of the current item of `units()` units.
+// Walks the pieces of a worker's range in order: after begin(), while (more()), key tiles [t0, t1) of
+// item `item` (tokens [tok, tok + toks) of segment s, kv head `head`).  The starting cost of an item
+// lies before its first tile, and a range that ends within it leaves the item to the next worker.
 struct PagedWalk {
   PagedSeg s;
-  int seg, head, item, items, n_units;
-  long long u, u1, item_u0;
+  int seg, head, index, items;        // index: among the items of the kind
+  int item, tok, toks, keys, tiles;   // the current item; keys it visits
+  int t0, t1;
+  int kind;
+  long long u1, item_u0, u;
 
-  DG_HD void begin(const PagedShape &p, const PagedStart &st) {
+  DG_HD void begin(const PagedShape &p, int kind_, const PagedStart &st) {
+    kind = kind_;
     seg = st.seg;
     head = st.head;
-    item = st.item;
+    index = st.item;
     u = st.u0;
     u1 = st.u1;
     item_u0 = st.item_u0;
-    if (!more()) return;
+    if (u >= u1) return;
     s = paged_seg(p, seg);
-    items = paged_items(p, s);
-    n_units = paged_item_units(p, s, item);
+    items = paged_items(p, s, kind);
+    load(p);
+    if (t0 >= t1) next(p);
   }
   DG_HD bool more() const { return u < u1; }
-  DG_HD int units() const { return n_units; }
-  DG_HD int k0() const { return (int)(u - item_u0); }
-  DG_HD int k1() const { return u1 - item_u0 < n_units ? (int)(u1 - item_u0) : n_units; }
+  DG_HD bool whole() const { return t0 == 0 && t1 == tiles; }
+  DG_HD void load(const PagedShape &p) {
+    item = paged_first_item(p, s, kind) + index;
+    tok = item * p.qt;
+    toks = paged_item_tokens(p, s, item);
+    keys = paged_item_keys(p, s, item);
+    tiles = (keys + p.kt[kind] - 1) / p.kt[kind];
+    const int c = p.start_cost[kind];
+    const long long a = u - item_u0 - c, b = u1 - item_u0 - c;
+    t0 = a > 0 ? (int)a : 0;
+    t1 = b < tiles ? (b > 0 ? (int)b : 0) : tiles;
+  }
   DG_HD void next(const PagedShape &p) {
-    item_u0 += n_units;
-    u = item_u0;  // past u1 when the piece ended inside its item
-    if (!more()) return;
-    if (++item == items) {
-      item = 0;
-      if (++head == p.Hkv) {
-        head = 0;
-        do {  // units remain, so a later segment has rows
-          s = paged_seg(p, ++seg);
-        } while (s.n == 0);
-        items = paged_items(p, s);
+    do {
+      item_u0 += tiles + p.start_cost[kind];
+      u = item_u0;
+      if (!more()) return;
+      if (++index == items) {
+        index = 0;
+        if (++head == p.Hkv) {
+          head = 0;
+          do {  // cost remains, so a later segment has items
+            s = paged_seg(p, ++seg);
+            items = s.n > 0 ? paged_items(p, s, kind) : 0;
+          } while (items == 0);
+        }
       }
-    }
-    n_units = paged_item_units(p, s, item);
+      load(p);
+    } while (t0 >= t1);
   }
 };
 
-// What CTA c leaves about the item that its range begins in, for joining the pieces.
+// What a worker leaves about the item that its range goes on with, for joining the pieces.
 struct PagedHead {
-  int joins;    // 1: the range begins inside an item, and is the first boundary inside it
-  int last;     // CTA that holds the item's last unit
+  int joins;    // 1: the range begins inside an item whose first piece lies with the worker before
+  int last;     // worker (of the kind) that holds the item's last tile
   int tok0, tokens, head;   // packed rows and kv head of the item
   int pad[3];
 };
+DG_HD PagedHead paged_head(const PagedShape &p, int kind, const PagedStart &st) {
+  PagedHead h = {0, 0, 0, 0, 0, {0, 0, 0}};
+  const int c = p.start_cost[kind];
+  const long long in = st.u0 - st.item_u0;
+  if (st.u0 < st.u1 && in > c) {
+    const PagedSeg s = paged_seg(p, st.seg);
+    const int item = paged_first_item(p, s, kind) + st.item;
+    const long long end = st.item_u0 + c + paged_item_tiles(p, s, kind, item);
+    h.joins = in - st.per <= c;
+    h.last = (int)((end - 1) / st.per);
+    h.tok0 = s.tok0 + item * p.qt;
+    h.tokens = paged_item_tokens(p, s, item);
+    h.head = st.head;
+  }
+  return h;
+}
 
 }  // namespace dg

@@ -40,13 +40,14 @@ int make_tmap_2d(CUtensorMap *out, CUtensorMapDataType dtype, int elem_bytes, co
 }
 
 int make_tmap_3d(CUtensorMap *out, CUtensorMapDataType dtype, int elem_bytes, const void *base,
-                 uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1, uint32_t b2) {
+                 uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0,
+                 uint32_t b1, uint32_t b2) {
   std::call_once(g_encode_once, load_encode);
   if (!g_encode) return DG_ERR_CUDA;
-  if (((uintptr_t)base & 15) || ((d0 * elem_bytes) & 15) || ((b0 * elem_bytes) & 15))
+  if (((uintptr_t)base & 15) || (s1 & 15) || (s2 & 15) || ((b0 * elem_bytes) & 15))
     return DG_ERR_INVALID_ARG;
   cuuint64_t dims[3] = {d0, d1, d2};
-  cuuint64_t strides[2] = {d0 * elem_bytes, d0 * d1 * elem_bytes};
+  cuuint64_t strides[2] = {s1, s2};
   cuuint32_t box[3] = {b0, b1, b2};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = g_encode(out, dtype, 3, const_cast<void *>(base), dims, strides, box, estr,

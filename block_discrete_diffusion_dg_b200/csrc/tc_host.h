@@ -12,10 +12,11 @@ int make_tmap_2d(CUtensorMap *out, CUtensorMapDataType dtype, int elem_bytes, co
                  uint64_t inner, uint64_t rows, uint64_t row_stride_bytes, uint32_t box_inner,
                  uint32_t box_rows);
 
-// 3-D tensor map over dense [d2][d1][d0] (d0 contiguous) with the 128-byte swizzle, box
-// [b2][b1][b0].  Out-of-range boxes read zeros.
+// 3-D tensor map over [d2][d1][d0] (d0 contiguous, the others s2 and s1 bytes apart) with the 128-byte
+// swizzle, box [b2][b1][b0].  Out-of-range boxes read zeros.
 int make_tmap_3d(CUtensorMap *out, CUtensorMapDataType dtype, int elem_bytes, const void *base,
-                 uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1, uint32_t b2);
+                 uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0,
+                 uint32_t b1, uint32_t b2);
 
 // 3-D tensor map over fp32 [d2][d1][d0] (d0 contiguous), no swizzle, box [b2][b1][b0]; for tiled
 // stores from shared memory laid out [b1][b0].

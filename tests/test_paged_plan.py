@@ -21,20 +21,21 @@ static int rnd(int n) { x ^= x << 13; x ^= x >> 7; x ^= x << 17; return (int)(x 
 struct Unit { int seg, head, item, k; };
 
 // The range start as paged_locate finds it, by plain counting.
-static PagedStart locate(const PagedShape &p, int cta, int ctas) {
+static PagedStart locate(const PagedShape &p, int kind, int worker, int workers) {
   long long total = 0;
-  for (int i = 0; i < paged_segs(p); ++i) total += paged_seg_units(p, paged_seg(p, i));
+  for (int i = 0; i < paged_segs(p); ++i) total += p.Hkv * paged_head_cost(p, paged_seg(p, i), kind);
   PagedStart r{};
-  r.per = (total + ctas - 1) / ctas;
-  r.u0 = cta * r.per;
+  r.per = (total + workers - 1) / workers;
+  if (r.per < p.least[kind]) r.per = p.least[kind];
+  r.u0 = worker * r.per;
   r.u1 = r.u0 + r.per < total ? r.u0 + r.per : total;
   if (r.u0 >= r.u1) { r.u0 = r.u1 = 0; return r; }
   long long at = 0;
   for (int i = 0; i < paged_segs(p); ++i) {
     const PagedSeg s = paged_seg(p, i);
     for (int h = 0; s.n > 0 && h < p.Hkv; ++h)
-      for (int q = 0; q < paged_items(p, s); ++q) {
-        const int n = paged_item_units(p, s, q);
+      for (int q = 0; q < paged_items(p, s, kind); ++q) {
+        const int n = p.start_cost[kind] + paged_item_tiles(p, s, kind, paged_first_item(p, s, kind) + q);
         if (r.u0 >= at && r.u0 < at + n) { r.seg = i; r.head = h; r.item = q; r.item_u0 = at; return r; }
         at += n;
       }
@@ -54,12 +55,18 @@ int main() {
     const bool wide = rnd(2);
     PagedShape p{};
     p.Hkv = 1 + rnd(4);
-    p.kt = wide ? 128 : 64;
+    p.kt[0] = p.kt[1] = wide ? 128 : 64;
+    p.kt[2] = 16;
+    for (int k = 0; k < 3; ++k) p.least[k] = rnd(2) ? rnd(9) : 0;
     p.qt = (wide ? 128 : 64) / rep * (wide ? 2 : 1);
     p.qn = wide ? 128 / rep : 0;
+    p.qf = wide && rnd(2) ? 16 / rep : 0;
     p.causal = rnd(2);
     p.shared_len = rnd(3) ? 0 : page * (1 + rnd(20));
     p.cap = p.shared_len + 100000;
+    p.start_cost[0] = rnd(4);
+    p.start_cost[1] = rnd(4);
+    p.start_cost[2] = rnd(4);
     std::vector<int> off(1, 0), kv;
     for (int s = 0; s < seqs; ++s) {
       off.push_back(off.back() + (rnd(4) ? (rnd(2) ? 1 : rnd(700)) : 0));
@@ -70,49 +77,88 @@ int main() {
     p.n_seqs = seqs;
     p.n_tokens = off.back() + rnd(5);
     if (p.n_tokens == 0) p.n_tokens = 1;
-    std::vector<Unit> all;
-    for (int i = 0; i < paged_segs(p); ++i) {
-      const PagedSeg s = paged_seg(p, i);
-      CHECK(s.error == 0);
-      if (s.n == 0) { CHECK(paged_seg_units(p, s) == 0); continue; }
-      long long before = 0;
-      for (int q = 0; q < paged_items(p, s); ++q) {
-        CHECK(paged_units_before(p, s, q) == before);
-        CHECK(paged_item_units(p, s, q) > 0);
-        const int span = paged_item_tokens(p, s, q) <= p.qn ? 2 * p.kt : p.kt;
-        CHECK(paged_item_units(p, s, q) * (long long)span >= paged_item_keys(p, s, q));
-        CHECK((paged_item_units(p, s, q) - 1) * (long long)span < paged_item_keys(p, s, q));
-        before += paged_item_units(p, s, q);
-      }
-      CHECK(paged_units_before(p, s, paged_items(p, s)) == before);
-      for (int h = 0; h < p.Hkv; ++h)
-        for (int q = 0; q < paged_items(p, s); ++q)
-          for (int k = 0; k < paged_item_units(p, s, q); ++k) all.push_back({i, h, q, k});
-    }
-    const int ctas = rnd(2) ? 148 : 1 + rnd(300);
-    size_t at = 0;
-    for (int c = 0; c < ctas; ++c) {
-      const PagedStart st = locate(p, c, ctas);
-      PagedWalk w;
-      int pieces = 0, cont = 0;
-      for (w.begin(p, st); w.more(); w.next(p)) {
-        CHECK(w.k0() < w.k1() && w.k1() <= w.units());
-        cont += w.k0() > 0;
-        CHECK(w.k0() == 0 || pieces == 0);                       // only the first piece goes on
-        CHECK(w.k1() == w.units() || w.u + (w.k1() - w.k0()) == st.u1);   // only the last is cut
-        for (int k = w.k0(); k < w.k1(); ++k, ++at) {
-          CHECK(at < all.size());
-          CHECK(all[at].seg == w.seg && all[at].head == w.head && all[at].item == w.item && all[at].k == k);
+    for (int kind = 0; kind < 3; ++kind) {
+      std::vector<Unit> all;
+      for (int i = 0; i < paged_segs(p); ++i) {
+        const PagedSeg s = paged_seg(p, i);
+        CHECK(s.error == 0);
+        if (s.n == 0) { CHECK(paged_head_cost(p, s, kind) == 0); continue; }
+        const int first = paged_first_item(p, s, kind), n = paged_items(p, s, kind);
+        if (kind == 0) {   // every token in one item of one kind
+          int rows = 0;
+          for (int q = 0; q < n; ++q) rows += paged_item_tokens(p, s, q);
+          const int tail = paged_tail_kind(p, s);
+          for (int k = 1; k < 3; ++k) {
+            CHECK(paged_items(p, s, k) == (tail == k ? 1 : 0));
+            if (tail == k) CHECK(paged_first_item(p, s, k) == n);
+          }
+          if (tail) {
+            const int last = paged_item_tokens(p, s, n);
+            CHECK(last > 0 && last <= p.qn && (tail == 2) == (last <= p.qf));
+            rows += last;
+          } else {
+            CHECK(paged_item_tokens(p, s, n - 1) > p.qn);
+          }
+          CHECK(rows == s.n);
         }
-        ++pieces;
+        long long before = 0;
+        for (int q = 0; q < n; ++q) {
+          CHECK(paged_cost_before(p, s, kind, q) == before);
+          const int t = paged_item_tiles(p, s, kind, first + q);
+          CHECK(t > 0 && t * (long long)p.kt[kind] >= paged_item_keys(p, s, first + q));
+          CHECK((t - 1) * (long long)p.kt[kind] < paged_item_keys(p, s, first + q));
+          before += t + p.start_cost[kind];
+        }
+        CHECK(paged_cost_before(p, s, kind, n) == before && paged_head_cost(p, s, kind) == before);
+        for (int h = 0; h < p.Hkv; ++h)
+          for (int q = 0; q < n; ++q)
+            for (int k = 0; k < paged_item_tiles(p, s, kind, first + q); ++k)
+              all.push_back({i, h, first + q, k});
       }
+      const int workers = rnd(2) ? 148 : 1 + rnd(300);
+      size_t at = 0;
+      std::vector<int> begun(workers, -1);   // the cut item that begins with a worker
+      int open = -1, open_tiles = 0;         // worker where the item now being cut began
+      long long open_last = -1;
+      for (int c = 0; c < workers; ++c) {
+        const PagedStart st = locate(p, kind, c, workers);
+        const PagedHead hd = paged_head(p, kind, st);
+        PagedWalk w;
+        int pieces = 0, slots[2] = {0, 0};
+        bool goes_on = false;
+        for (w.begin(p, kind, st); w.more(); w.next(p)) {
+          CHECK(w.t0 < w.t1 && w.t1 <= w.tiles);
+          CHECK(w.t0 == 0 || pieces == 0);                       // only the first piece goes on
+          if (!w.whole()) ++slots[w.t0 == 0];
+          for (int k = w.t0; k < w.t1; ++k, ++at) {
+            CHECK(at < all.size());
+            CHECK(all[at].seg == w.seg && all[at].head == w.head && all[at].item == w.item && all[at].k == k);
+          }
+          if (w.t0 > 0) {
+            goes_on = true;
+            CHECK(open >= 0 && hd.joins == (open == c - 1));
+            CHECK(hd.tok0 == w.s.tok0 + w.tok && hd.tokens == w.toks && hd.head == w.head);
+            if (open_last < 0) open_last = hd.last;
+            CHECK(open_last == hd.last);
+            if (w.t1 == w.tiles) { CHECK(hd.last == c); open = -1; }
+          }
+          if (w.t0 == 0 && !w.whole()) {
+            CHECK(open < 0);
+            open = c; open_last = -1; open_tiles = w.tiles;
+          }
+          ++pieces;
+        }
+        (void)open_tiles;
+        if (!goes_on) CHECK(hd.joins == 0);
+        CHECK(slots[0] <= 1 && slots[1] <= 1);
+      }
+      CHECK(at == all.size() && open < 0);
     }
-    CHECK(at == all.size());
   }
   // error codes
   int off[] = {0, 4, 2, 9, 12, 12}, kv[] = {5, 5, -1, 97, 1000000};
   PagedShape p{};
-  p.seq_off = off; p.kv_len = kv; p.n_seqs = 5; p.n_tokens = 12; p.Hkv = 1; p.qt = 64; p.kt = 64; p.cap = 99;
+  p.seq_off = off; p.kv_len = kv; p.n_seqs = 5; p.n_tokens = 12; p.Hkv = 1; p.qt = 64; p.kt[0] = 64; p.cap = 99;
   CHECK(paged_seg(p, 0).error == 0 && paged_seg(p, 0).n == 4 && paged_seg(p, 0).keys == 9);
   CHECK(paged_seg(p, 1).error == 1 && paged_seg(p, 1).n == 0);       // descending offsets
   CHECK(paged_seg(p, 2).error == 1 && paged_seg(p, 2).n == 0);       // negative length
