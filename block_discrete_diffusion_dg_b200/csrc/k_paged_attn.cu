@@ -45,19 +45,13 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(PagedShape p,
   constexpr int DPT = HD / 16, VEC = DPT < 4 ? DPT : 4, NV = DPT / VEC;
   extern __shared__ __align__(16) float simt_smem_raw[];
   float *Qs = simt_smem_raw, *KVs = Qs + S_ROWS * LD, *Ps = KVs + S_KT * LD;
-  __shared__ PagedStart start_s;
+  __shared__ PagedStart start[1];
+  __shared__ PagedScan scan;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  if (tid < 32) {
-    int err;
-    const PagedStart st = paged_locate(p, PAGED_WIDE, blockIdx.x, gridDim.x, &err);
-    if (tid == 0) {
-      start_s = st;
-      if (blockIdx.x == 0) paged_report(io, err);
-      io.heads[blockIdx.x] = paged_head(p, PAGED_WIDE, st);
-    }
-  }
+  const int err = paged_locate<S_THR>(p, blockIdx.x, gridDim.x, 1, start, io.heads, scan);
   __syncthreads();
-  const PagedStart st = start_s;
+  const PagedStart st = start[0];
+  if (tid == 0 && blockIdx.x == 0) paged_report(io, err);
   const int rep = io.rep;
   const float sl2 = 1.4426950408889634f * rsqrtf((float)HD);
   PagedWalk w;
@@ -241,15 +235,13 @@ struct Fold {
       }
     }
   }
-  // Row r of the item whose pieces lie with workers first .. last (the item begins at `first`).
-  // (`last` counted within their kind).
-  __device__ __forceinline__ void add_pieces(const PagedIO &io, int first, int last, int r) {
+  // Row r of the item that begins at worker `begin`, its pieces with workers first .. last.
+  __device__ __forceinline__ void add_range(const PagedIO &io, int begin, int first, int last, int r) {
     const int lane = threadIdx.x & 31;
-    last += paged_first_worker(io, paged_worker_kind(io, first));
     for (int c0 = first; c0 <= last; c0 += 32) {
       const int n = min(32, last - c0 + 1);
       const int c = c0 + min(lane, n - 1);
-      const size_t row = paged_slot_row(io, c, c == first, r);
+      const size_t row = paged_slot_row(io, c, c == begin, r);
       add(io.part_o, n, io.part_ml[row], row);
     }
   }
@@ -261,74 +253,201 @@ struct Fold {
   }
 };
 
-// Joins the items that range boundaries cut: worker c acts where it is the second to work on the item
-// that its range begins in.  A warp per row; a block takes one worker and a share of its rows (the
-// first `blocks` of them: wide items 8 shares, narrow ones 1), or eight workers of few-row items.
-struct JoinGrid {
-  int wide, narrow, few;   // blocks
-};
+// NR rows at once, each of NS partial results (NR x NS loads in flight).  row[i][k]: rows of part_o, on:
+// whether they count; dst[i]: output row, or null.
+template <typename T, int HD, int NR, int NS>
+__device__ __forceinline__ void join_some(const PagedIO &io, const size_t (&row)[NR][NS],
+                                          const bool (&on)[NR][NS], T *const (&dst)[NR]) {
+  constexpr int V = HD / 32;
+  const int lane = threadIdx.x & 31;
+  float2 ml[NR][NS];
+  float x[NR][NS][V];
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      ml[i][k] = io.part_ml[row[i][k]];
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[i][k][v] = io.part_o[row[i][k] * HD + lane * V + v];
+    }
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    if (!dst[i]) continue;
+    float m = -INFINITY, l = 0.f, y[V] = {};
+#pragma unroll
+    for (int k = 0; k < NS; ++k)
+      if (on[i][k]) m = fmaxf(m, ml[i][k].x);
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      if (!on[i][k]) continue;
+      const float c = exp2f(ml[i][k].x - base);
+      l = fmaf(ml[i][k].y, c, l);
+#pragma unroll
+      for (int v = 0; v < V; ++v) y[v] = fmaf(x[i][k][v], c, y[v]);
+    }
+    const float il = l > 0.f ? 1.f / l : 0.f;
+    T *d = dst[i] + lane * V;
+    if constexpr (V == 4) store4<T>(d, y[0] * il, y[1] * il, y[2] * il, y[3] * il);
+    else
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] = from_f<T>(y[v] * il);
+  }
+}
+
+// Joins the items that range boundaries cut.  The workers that go on with an item share its rows: of
+// wide and narrow items each has two blocks, of few-row ones eight have one.  Where an item of few rows
+// was cut for many workers (one long context), the warps of a block share the pieces of a row and join
+// once more through shared memory; else a warp takes whole rows.
+// (Blocks are few on purpose: most have nothing to do, and a thousand of them cost more than the
+// joining.)
 template <typename T, int HD>
-__global__ void __launch_bounds__(256) paged_join_kernel(PagedIO io, JoinGrid g) {
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedIO io, int first) {
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5;
-  int b = blockIdx.x, c, r, step;
-  if (b < g.wide) {
-    c = b / 8;
-    r = b % 8 * 8 + warp;
-    step = 64;
-  } else if ((b -= g.wide) < g.narrow) {
-    c = io.ctas + b;
-    r = warp;
-    step = 8;
-  } else {
-    c = 3 * io.ctas + (b - g.narrow) * 8 + warp;
-    r = 0;
-    step = 1;
+  __shared__ float acc_s[8][HD];
+  __shared__ float2 ml_s[8];
+  constexpr int MANY = 16;   // pieces worth sharing
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wide = 3 * io.ctas - first;   // workers with two blocks, from `first` on
+  const bool few = (int)blockIdx.x >= 2 * wide;
+  const int c0 = few ? 3 * io.ctas + (blockIdx.x - 2 * wide) * 8 : first + blockIdx.x / 2;
+  const int c = few ? c0 + warp : c0, base = paged_first_worker(io, paged_worker_kind(io, c));
+  auto out = [&](const PagedHead &h, int r) {
+    return (T *)io.out + ((size_t)(h.tok0 + r / io.rep) * io.Hq + h.head * io.rep + r % io.rep) * HD;
+  };
+  {
+    const PagedHead h = io.heads[c];
+    const int rows = h.first >= 0 ? h.tokens * io.rep : 0, n = h.last - h.first + 1;
+    const int begin = base + h.first;
+    // this warp's rows r0, r0 + step, ... of the item's shares
+    int r0 = c - begin - 1, step = n - 1;
+    if (!few) {
+      r0 = (r0 * 2 + (blockIdx.x & 1)) * 8 + warp;
+      step *= 16;
+    }
+    if (n == 2) {
+      constexpr int NR = 4;
+#pragma unroll 1
+      for (; r0 < rows; r0 += NR * step) {
+        size_t row[NR][2];
+        bool on[NR][2];
+        T *dst[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const int r = r0 + i * step, rr = min(r, rows - 1);
+          row[i][0] = paged_slot_row(io, begin, true, rr);
+          row[i][1] = paged_slot_row(io, begin + 1, false, rr);
+          on[i][0] = on[i][1] = true;
+          dst[i] = r < rows ? out(h, r) : nullptr;
+        }
+        join_some<T, HD, NR, 2>(io, row, on, dst);
+      }
+    } else if (!few || n <= MANY) {
+#pragma unroll 1
+      for (; r0 < rows; r0 += step) {
+        Fold<HD> f;
+        f.add_range(io, begin, begin, begin + n - 1, r0);
+        f.store(out(h, r0));
+      }
+    }
   }
-  const PagedHead h = io.heads[c];
-  if (!h.joins) return;
-  const int rows = h.tokens * io.rep;
-  for (; r < rows; r += step) {
-    Fold<HD> f;
-    f.add_pieces(io, c - 1, h.last, r);
-    f.store((T *)io.out +
-            ((size_t)(h.tok0 + r / io.rep) * io.Hq + h.head * io.rep + r % io.rep) * HD);
+  if (!few) return;
+  // few-row items of many pieces: this block's part of their rows
+#pragma unroll 1
+  for (int w = 0; w < 8; ++w) {
+    const PagedHead h = io.heads[c0 + w];
+    const int n = h.last - h.first + 1, begin = base + h.first;
+    // once per block and item: with the first of the block's workers that goes on with it
+    if (h.first < 0 || n <= MANY || (w > 0 && begin < c0 + w - 1)) continue;
+    // blocks that hold such workers
+    const int b0 = (begin + 1 - 3 * io.ctas) / 8, b1 = (begin + n - 1 - 3 * io.ctas) / 8;
+    const int rows = h.tokens * io.rep, per = (n + 7) / 8;
+    const int p0 = min(warp * per, n), p1 = min(p0 + per, n);
+    for (int r = (c0 - 3 * io.ctas) / 8 - b0; r < rows; r += b1 - b0 + 1) {
+      Fold<HD> f;
+      f.add_range(io, begin, begin + p0, begin + p1 - 1, r);
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < Fold<HD>::V; ++v) acc_s[warp][lane * Fold<HD>::V + v] = f.acc[v];
+      if (lane == 0) ml_s[warp] = make_float2(f.m, f.l);
+      __syncthreads();
+      if (warp == 0) {
+        Fold<HD> g;
+        g.add(&acc_s[0][0], 8, ml_s[min(lane, 7)], min(lane, 7));
+        g.store(out(h, r));
+      }
+    }
   }
 }
 
 // Joins each row's result over the shared prefix with the one over its own keys; either may have
-// been cut into pieces.  A block per packed row, a warp per query head.
+// been cut into pieces.  A warp takes two query heads of a packed row.
 template <typename T, int HD>
 __global__ void __launch_bounds__(256) paged_join_prefix_kernel(PagedShape p, PagedIO io) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int live;
-  const int tok = blockIdx.x;
-  if (threadIdx.x == 0) {
-    // the sequence that holds this row, if it is one the attention took
-    int lo = 0, hi = p.n_seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (p.seq_off[mid] <= tok) lo = mid;
-      else hi = mid;
-    }
-    const PagedSeg s = paged_seg(p, lo + 1);
-    live = s.n > 0 && tok >= s.tok0 && tok < s.tok0 + s.n;
+  constexpr int NR = 2, NS = 4;
+  const int groups = (io.Hq + NR - 1) / NR;
+  const long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int tok = (int)(task / groups), h0 = (int)(task % groups) * NR;
+  if (tok >= p.n_tokens) return;
+  // what the region says of the rows, while the sequence is searched
+  float2 ml[NR][2];
+#pragma unroll
+  for (int i = 0; i < NR; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      ml[i][k] = io.part_ml[paged_region_row(p, io, k, tok, min(h0 + i, io.Hq - 1))];
+  // the sequence that holds this row, if it is one the attention took
+  int lo = 0, hi = p.n_seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (p.seq_off[mid] <= tok) lo = mid;
+    else hi = mid;
   }
-  __syncthreads();
-  if (!live) return;
-  for (int h = threadIdx.x >> 5; h < io.Hq; h += 8) {
-    Fold<HD> f;
-    for (int which = 0; which < 2; ++which) {
-      const size_t row = paged_region_row(p, io, which, tok, h);
-      const float2 ml = io.part_ml[row];
-      if (ml.y < 0.f) {  // cut into pieces from this worker on
-        const int c = __float_as_int(ml.x);
+  const PagedSeg s = paged_seg(p, lo + 1);
+  if (s.n == 0 || tok < s.tok0 || tok >= s.tok0 + s.n) return;
+  size_t row[NR][NS];
+  bool on[NR][NS], many = false;
+  T *dst[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int h = min(h0 + i, io.Hq - 1);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      row[i][2 * k] = row[i][2 * k + 1] = paged_region_row(p, io, k, tok, h);
+      on[i][2 * k] = true;
+      on[i][2 * k + 1] = ml[i][k].y < 0.f;
+      if (ml[i][k].y < 0.f) {  // cut into pieces from this worker on
+        const int c = __float_as_int(ml[i][k].x);
         const PagedHead hd = io.heads[c + 1];
-        f.add_pieces(io, c, hd.last, (tok - hd.tok0) * io.rep + h % io.rep);
+        many = many || hd.last > hd.first + 1;
+        const int r = (tok - hd.tok0) * io.rep + h % io.rep;
+        row[i][2 * k] = paged_slot_row(io, c, true, r);
+        row[i][2 * k + 1] = paged_slot_row(io, c + 1, false, r);
+      }
+    }
+    dst[i] = h0 + i < io.Hq ? (T *)io.out + ((size_t)tok * io.Hq + h) * HD : nullptr;
+  }
+  if (!many) {
+    join_some<T, HD, NR, NS>(io, row, on, dst);
+    return;
+  }
+#pragma unroll 1
+  for (int h = h0; h < min(h0 + NR, io.Hq); ++h) {
+    Fold<HD> f;
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const size_t r = paged_region_row(p, io, which, tok, h);
+      const float2 e = io.part_ml[r];
+      if (e.y < 0.f) {
+        const int c = __float_as_int(e.x);
+        const PagedHead hd = io.heads[c + 1];
+        f.add_range(io, c, c, hd.last + paged_first_worker(io, paged_worker_kind(io, c)),
+                    (tok - hd.tok0) * io.rep + h % io.rep);
       } else {
-        f.add(io.part_o, 1, ml, row);
+        f.add(io.part_o, 1, e, r);
       }
     }
     f.store((T *)io.out + ((size_t)tok * io.Hq + h) * HD);
@@ -348,16 +467,16 @@ template <typename T, int HD>
 int run_join(const PagedShape &p, const PagedIO &io, cudaStream_t s) {
   if (p.shared_len > 0) {
     note_launch(s, "paged_join_prefix");
-    launch_pdl(paged_join_prefix_kernel<T, HD>, p.n_tokens, 256, 0, s, p, io);
+    const long long tasks = (long long)p.n_tokens * ((io.Hq + 1) / 2);
+    launch_pdl(paged_join_prefix_kernel<T, HD>, (unsigned)((tasks + 7) / 8), 256, 0, s, p, io);
     return check_launch("paged_join_prefix");
   }
   // no item of a kind can exist with fewer rows than it takes
-  JoinGrid g{0, 0, 0};
-  if (p.n_tokens > p.qn) g.wide = 8 * io.ctas;
-  if (p.qn > 0 && p.n_tokens > p.qf) g.narrow = 2 * io.ctas;
-  if (p.qf > 0) g.few = io.ctas;
+  const bool tc = io.workers > io.ctas;
+  const int first = !tc || p.n_tokens > p.qn ? 0 : p.n_tokens > p.qf ? io.ctas : 3 * io.ctas;
+  const int blocks = tc ? 2 * (3 * io.ctas - first) + io.ctas : 2 * io.ctas;
   note_launch(s, "paged_join");
-  launch_pdl(paged_join_kernel<T, HD>, g.wide + g.narrow + g.few, 256, 0, s, io, g);
+  launch_pdl(paged_join_kernel<T, HD>, blocks, 256, 0, s, io, first);
   return check_launch("paged_join");
 }
 
@@ -371,8 +490,13 @@ void paged_tiling(const PagedCall &c, PagedShape *p, PagedIO *io) {
   p->qt = tile / rep * (tc ? 2 : 1);
   p->qn = tc ? tile / rep : 0;
   p->qf = tc ? PAGED_TC_FEW / rep : 0;
-  p->kt[PAGED_WIDE] = p->kt[PAGED_NARROW] = tc ? PAGED_TC_KT : S_KT;
-  p->kt[PAGED_FEW] = PAGED_TC_FEW_KT;
+  auto log2 = [](int v) {
+    int s = 0;
+    while ((1 << s) < v) ++s;
+    return s;
+  };
+  p->kt_shift[PAGED_WIDE] = p->kt_shift[PAGED_NARROW] = log2(tc ? PAGED_TC_KT : S_KT);
+  p->kt_shift[PAGED_FEW] = log2(PAGED_TC_FEW_KT);
   p->start_cost[PAGED_WIDE] = tc ? PAGED_TC_START_WIDE : 0;
   p->start_cost[PAGED_NARROW] = PAGED_TC_START_NARROW;
   p->start_cost[PAGED_FEW] = PAGED_TC_START_FEW;
@@ -426,6 +550,7 @@ int launch_paged_attn(const PagedCall &c, void *ws, cudaStream_t s) {
   p.causal = c.causal;
   p.shared_len = c.shared_len;
   p.cap = c.max_pages * c.page_size;
+  if (paged_cost_bound(p) > PAGED_COST_LIMIT) return DG_ERR_UNSUPPORTED;
   io.q = c.q;
   io.out = c.out;
   io.k_pages = c.k_pages;

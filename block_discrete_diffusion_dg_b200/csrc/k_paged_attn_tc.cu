@@ -13,8 +13,10 @@
 //                  the start and end of one's items hide behind the other's work.
 // Few-row items (single tokens: up to 16 rows) would leave 7/8 of such a tile empty and pass each key
 // tile through a chain of four waits; there each of the eight softmax warps walks a range of its own
-// with mma.sync, 16 keys a step, from a ring of its own in the memory that the chains have left, so
-// that almost all of it is in flight: these items are bound by the bytes of their keys.
+// with mma.sync, 32 keys a step, from a ring of its own in the memory that the chains have left, so
+// that almost all of it is in flight: these items are bound by the bytes of their keys.  Their copies
+// are cp.async, not TMA: a box of one 16-key page takes the TMA unit about 60 cycles for 2 KB, and eight
+// warps that each wait for several such boxes waited 3 us before their first product.
 // Tensor memory (512 columns): S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512); P_x is
 // written over S_x.  MMAs of one thread execute in issue order, so S_x of the next key tile is
 // issued right behind P_x V.
@@ -53,7 +55,7 @@ static_assert(128 * P_REGS_LO + 256 * P_REGS_HI <= P_THR * P_REGS, "register spl
 static_assert(P_THR * P_REGS <= 65536, "launch registers");
 
 constexpr int F_KT = PAGED_TC_FEW_KT;      // few-row items: keys per step,
-constexpr int F_SLOTS = 6;                 // K and V slots of a warp's ring (three steps)
+constexpr int F_SLOTS = 3;                 // slots of a warp's ring, K and V of a step in turn
 
 template <int HD>
 struct Tc {
@@ -61,7 +63,7 @@ struct Tc {
   static constexpr int TILE = HALVES * P_HALF;          // 128 rows x HD
   static constexpr int STAGES = HD == 128 ? 4 : 8;      // key and value tiles in flight
   static_assert(8 * F_SLOTS * F_KT * HD * 2 <= (2 + STAGES) * TILE, "few-row rings");
-  static constexpr size_t SMEM = 1024 + (size_t)TILE * (2 + STAGES) + 8 * P_STAGE + 1024;
+  static constexpr size_t SMEM = 1024 + (size_t)TILE * (2 + STAGES) + 8 * P_STAGE + 2048;
 };
 
 template <int R>
@@ -104,6 +106,17 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// 16 bytes from global to shared memory; `on` false: zeros.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 // 3-D tiled load of the box at (x = element, y, z).
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int x,
                                             int y, int z) {
@@ -128,8 +141,6 @@ __global__ void __launch_bounds__(P_THR, 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV,
-                         const __grid_constant__ CUtensorMap tmKf,
-                         const __grid_constant__ CUtensorMap tmVf,
                          const __grid_constant__ PagedShape p, const __grid_constant__ PagedIO io) {
   pdl_wait();
   pdl_trigger();
@@ -145,11 +156,11 @@ __global__ void __launch_bounds__(P_THR, 1)
   uint64_t *q_empty = q_full + 2, *full = q_empty + 2, *empty = full + S;
   uint64_t *s_full = empty + S, *p_full = s_full + 2, *pv_done = p_full + 2, *o_empty = pv_done + 2;
   uint64_t *mma_fin = o_empty + 2;
-  uint64_t *chains_done = mma_fin + 1, *f_full = chains_done + 1;        // [8][F_SLOTS]
-  PagedStart *start = reinterpret_cast<PagedStart *>(f_full + 8 * F_SLOTS);   // wide, chain A, chain B
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 3);
+  uint64_t *chains_done = mma_fin + 1;
+  PagedStart *start = reinterpret_cast<PagedStart *>(chains_done + 1);   // [PAGED_STARTS]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + PAGED_STARTS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert((4 + 2 * S + 10 + 8 * F_SLOTS) * 8 + 3 * sizeof(PagedStart) + 8 <= 1024, "shared memory");
+  static_assert((4 + 2 * S + 10) * 8 + PAGED_STARTS * sizeof(PagedStart) + 8 <= 2048, "shared memory");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 1) {
@@ -168,44 +179,25 @@ __global__ void __launch_bounds__(P_THR, 1)
       }
       mbar_init(mma_fin, 1);
       mbar_init(chains_done, 8);
-      for (int i = 0; i < 8 * F_SLOTS; ++i) mbar_init(&f_full[i], 1);
       *abort_flag = 0;
       fence_mbar_init();
     }
     __syncwarp();
     tmem_alloc(tmem_slot, P_TMEM);
     tmem_relinquish();
-  } else if (warp < 4) {
-    // warp 0 finds the range of wide items, warps 2 and 3 those of the chains' narrow items
-    const int kind = warp == 0 ? PAGED_WIDE : PAGED_NARROW;
-    const int worker = warp == 0 ? blockIdx.x : 2 * blockIdx.x + warp - 2;
-    int err;
-    const PagedStart st =
-        paged_locate(p, kind, worker, kind == PAGED_WIDE ? gridDim.x : 2 * gridDim.x, &err);
-    if (lane == 0) {
-      start[warp == 0 ? 0 : warp - 1] = st;
-      if (blockIdx.x == 0 && warp == 0) paged_report(io, err);
-      io.heads[paged_first_worker(io, kind) + worker] = paged_head(p, kind, st);
-    }
+  } else if (warp == 2 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
-  PagedStart few_start{};
-  if (warp >= 4) {
-    if (warp == 4 && lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-      tma_prefetch_desc(&tmKf);
-      tma_prefetch_desc(&tmVf);
-    }
-    int err;
-    const int worker = 8 * blockIdx.x + warp - 4;
-    few_start = paged_locate(p, PAGED_FEW, worker, 8 * gridDim.x, &err);
-    if (lane == 0) io.heads[paged_first_worker(io, PAGED_FEW) + worker] = paged_head(p, PAGED_FEW, few_start);
-  }
+  // (the scan's scratch lies where rows will leave the kernel much later)
+  const int err = paged_locate<P_THR / 3>(p, blockIdx.x, gridDim.x, PAGED_STARTS, start, io.heads,
+                                          *reinterpret_cast<PagedScan *>(sOut));
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (threadIdx.x == 0 && blockIdx.x == 0) paged_report(io, err);
   const int rep = io.rep, qn = p.qn;   // qn tokens of rep heads make a query tile
 
   if (warp == 0) {
@@ -539,7 +531,7 @@ __global__ void __launch_bounds__(P_THR, 1)
         fence_after();
         if (warp_on) {
           const int worker = paged_first_worker(io, kind) +
-                             (kind == PAGED_WIDE ? (int)blockIdx.x : 2 * (int)blockIdx.x + x);
+                             (kind == PAGED_WIDE ? 0 : x * io.ctas) + (int)blockIdx.x;
           const PagedDest dest = paged_dest(p, io, w, worker);
           const int on = min(32, rows - q4 * 32);       // rows of this warp
           const bool out = dest.kind == PAGED_OUT;
@@ -594,86 +586,73 @@ __global__ void __launch_bounds__(P_THR, 1)
     // this warp has left its chain; when all eight have, the rings and query tiles are idle
     __syncwarp();
     if (lane == 0) mbar_arrive(chains_done);
+    const PagedStart &few_start = start[3 + warp - 4];
     if (ok && few_start.u0 < few_start.u1) {
-      constexpr int SLOT = F_KT * HD * 2;                       // 16 keys: [half][16 rows][128 bytes]
+      constexpr int ROW = HD * 2, SLOT = F_KT * ROW;            // a slot: 32 keys, chunks swizzled
       const int fw = warp - 4, gr = lane >> 2, tq = lane & 3;   // fragment row and column pair
       uint8_t *ring = sQ + fw * F_SLOTS * SLOT;
-      uint64_t *bar = f_full + fw * F_SLOTS;
-      uint32_t issued = 0, taken = 0;                           // slots (K and V of a step in turn)
+      const int shift = io.page_shift;
       ok = __all_sync(FULL, mbar_wait(chains_done, 0));
-      // copies run F_SLOTS / 2 steps ahead of the arithmetic, across items; page ids one step further
-      PagedWalk lw;
-      int lt = 0, ly = 0;
-      auto lookup = [&]() {
-        const long long row = paged_row(io, p, lw.s.seq, lw.head, lw.s.key0 + lt * F_KT);
-        ly = row < 0 ? (io.n_pages * p.Hkv) << io.page_shift : (int)row;   // past the pool: zeros
-      };
-      auto issue = [&]() {
-        if (!lw.more()) return;
-        if (lane == 0) {
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t s = (issued + kv) % F_SLOTS;
-            mbar_expect_tx(&bar[s], SLOT);
-#pragma unroll
-            for (int h = 0; h < HALVES; ++h)
-              tma_load_2d(ring + s * SLOT + h * (F_KT * 128), kv ? &tmVf : &tmKf, &bar[s], h * 64, ly);
-          }
-        }
-        issued += 2;
-        if (++lt == lw.t1) {
-          lw.next(p);
-          lt = lw.t0;
-        }
-        if (lw.more()) lookup();
-      };
+      // Copies run F_SLOTS slots ahead of the arithmetic, across items: slot n of the walk is K (n even)
+      // or V of a step, one group of cp.async each.  Rows behind the last key are filled with zeros.
+      // Each lane holds the first row (for kv head 0) of a page, 32 pages of a sequence at a time.
+      PagedWalk lw, w;
       lw.begin(p, PAGED_FEW, few_start);
-      if (ok && lw.more()) {
-        lt = lw.t0;
-        lookup();
-        for (int i = 0; i < F_SLOTS / 2; ++i) issue();
-      }
-      PagedWalk w;
-      for (w.begin(p, PAGED_FEW, few_start); ok && w.more(); w.next(p)) {
-        const int rows = w.toks * rep, h0 = w.head * rep, tok_w = w.s.tok0 + w.tok;
-        uint32_t qf[HD / 16][4];   // Q as the A operand: rows gr and gr + 8
-        const bf16 *q0 = (const bf16 *)io.q + ((size_t)(tok_w + gr / rep) * io.Hq + h0 + gr % rep) * HD;
-        const bf16 *q1 = (const bf16 *)io.q +
-                         ((size_t)(tok_w + (gr + 8) / rep) * io.Hq + h0 + (gr + 8) % rep) * HD;
+      int lt = lw.t0, ids = 0, ids_seg = -1, ids_page = 0;
+      bool lv = false;
+      uint32_t ls_slot = 0, slot = 0;                           // slots loaded and used next
+      w.begin(p, PAGED_FEW, few_start);
+      int t = w.t0, lead = F_SLOTS;
+      bool v_half = false;
+      int seen[2] = {0, 0};                                     // keys that rows gr and gr + 8 see
+      uint32_t qf[HD / 16][4], ph[2][4], pl[2][4];
+      float o[HD / 8][4], m[2], ls[2];
+      while (ok) {
+        if (lead > 0) {
+          --lead;
+        } else if (!v_half) {
+          if (!w.more()) break;
+          const int rows = w.toks * rep, h0 = w.head * rep, tok_w = w.s.tok0 + w.tok;
+          if (t == w.t0) {   // an item's piece begins: Q as the A operand, rows gr and gr + 8
+            const bf16 *q0 =
+                (const bf16 *)io.q + ((size_t)(tok_w + gr / rep) * io.Hq + h0 + gr % rep) * HD + tq * 2;
+            const bf16 *q1 = (const bf16 *)io.q +
+                             ((size_t)(tok_w + (gr + 8) / rep) * io.Hq + h0 + (gr + 8) % rep) * HD + tq * 2;
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk) {
-          const int c = kk * 16 + tq * 2;
-          qf[kk][0] = gr < rows ? *reinterpret_cast<const uint32_t *>(q0 + c) : 0u;
-          qf[kk][1] = gr + 8 < rows ? *reinterpret_cast<const uint32_t *>(q1 + c) : 0u;
-          qf[kk][2] = gr < rows ? *reinterpret_cast<const uint32_t *>(q0 + c + 8) : 0u;
-          qf[kk][3] = gr + 8 < rows ? *reinterpret_cast<const uint32_t *>(q1 + c + 8) : 0u;
-        }
-        int seen[2];               // keys that rows gr and gr + 8 see
+            for (int kk = 0; kk < HD / 16; ++kk)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          seen[i] = w.s.causal ? w.s.keys - w.s.n + w.tok + min(gr + 8 * i, rows - 1) / rep + 1 : w.keys;
-        float o[HD / 8][4], m[2] = {-INFINITY, -INFINITY}, ls[2] = {0.f, 0.f};
+              for (int i = 0; i < 4; ++i)
+                qf[kk][i] = gr + 8 * (i & 1) < rows ? *reinterpret_cast<const uint32_t *>(
+                                                          (i & 1 ? q1 : q0) + kk * 16 + (i >> 1) * 8)
+                                                    : 0u;
 #pragma unroll
-        for (int j = 0; j < HD / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        for (int t = w.t0; t < w.t1; ++t, taken += 2) {
-          const int k0 = t * F_KT, live = min(F_KT, w.keys - k0);
-          const uint32_t ks = taken % F_SLOTS, vs = (taken + 1) % F_SLOTS;
-          if (!__all_sync(FULL, mbar_wait(&bar[ks], (taken / F_SLOTS) & 1))) { ok = false; break; }
-          float s[2][4] = {};
-          const uint8_t *K = ring + ks * SLOT;
+            for (int i = 0; i < 2; ++i) {
+              seen[i] = w.s.causal ? w.s.keys - w.s.n + w.tok + min(gr + 8 * i, rows - 1) / rep + 1 : w.keys;
+              m[i] = -INFINITY;
+              ls[i] = 0.f;
+            }
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            uint32_t b[4];
-            const int mi = lane >> 3, key = (mi >> 1) * 8 + (lane & 7);
-            const int chunk = (kk & 3) * 2 + (mi & 1);        // of the 8 chunks of a 128-byte row
-            ldsm_x4(b, K + (kk >> 2) * (F_KT * 128) + key * 128 + ((chunk ^ (key & 7)) << 4));
-            mma_16816(s[0], qf[kk], b[0], b[1]);
-            mma_16816(s[1], qf[kk], b[2], b[3]);
+            for (int j = 0; j < HD / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
           }
+          const int k0 = t * F_KT;
+          cp_wait<F_SLOTS - 1>();
+          __syncwarp();
+          float s[4][4] = {};
+          const uint8_t *K = ring + slot * SLOT;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+#pragma unroll
+            for (int nn = 0; nn < 2; ++nn) {
+              uint32_t b[4];
+              const int mi = lane >> 3, key = nn * 16 + (mi >> 1) * 8 + (lane & 7);
+              ldsm_x4(b, K + key * ROW + (((kk * 2 + (mi & 1)) ^ (key & 7)) << 4));
+              mma_16816(s[2 * nn], qf[kk], b[0], b[1]);
+              mma_16816(s[2 * nn + 1], qf[kk], b[2], b[3]);
+            }
           // rows gr (i = 0) and gr + 8: mask, running maximum, numerators
           float mt[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int key = k0 + j * 8 + tq * 2 + (e & 1);
@@ -703,9 +682,8 @@ __global__ void __launch_bounds__(P_THR, 1)
             }
           }
           // P as the A operand in two bf16 parts (16 significant bits; these products are cheap)
-          uint32_t ph[4], pl[4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float base = m[i] == -INFINITY ? 0.f : m[i];
@@ -714,69 +692,103 @@ __global__ void __launch_bounds__(P_THR, 1)
               const __nv_bfloat162 hi = __floats2bfloat162_rn(e0, e1);
               const __nv_bfloat162 lo =
                   __floats2bfloat162_rn(e0 - __low2float(hi), e1 - __high2float(hi));
-              ph[2 * j + i] = *reinterpret_cast<const uint32_t *>(&hi);
-              pl[2 * j + i] = *reinterpret_cast<const uint32_t *>(&lo);
+              ph[j >> 1][2 * (j & 1) + i] = *reinterpret_cast<const uint32_t *>(&hi);
+              pl[j >> 1][2 * (j & 1) + i] = *reinterpret_cast<const uint32_t *>(&lo);
             }
-          if (!__all_sync(FULL, mbar_wait(&bar[vs], ((taken + 1) / F_SLOTS) & 1))) { ok = false; break; }
-          uint8_t *V = ring + vs * SLOT;
-          if (live < F_KT) {   // rows past the last key: zeros, whatever they hold
-            for (int e = lane; e < (F_KT - live) * 8; e += 32)
+          v_half = true;
+          slot = slot + 1 == F_SLOTS ? 0 : slot + 1;
+        } else {
+          cp_wait<F_SLOTS - 1>();
+          __syncwarp();
+          const uint8_t *V = ring + slot * SLOT;
 #pragma unroll
-              for (int h = 0; h < HALVES; ++h)
-                reinterpret_cast<uint4 *>(V + h * (F_KT * 128) + live * 128)[e] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();   // before the copy that overwrites them later
-            __syncwarp();
-          }
+          for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-          for (int nn = 0; nn < HD / 16; ++nn) {
-            uint32_t b[4];
-            const int mi = lane >> 3, key = (mi & 1) * 8 + (lane & 7);
-            const int chunk = (nn & 3) * 2 + (mi >> 1);
-            ldsm_x4_t(b, V + (nn >> 2) * (F_KT * 128) + key * 128 + ((chunk ^ (key & 7)) << 4));
-            mma_16816(o[2 * nn], ph, b[0], b[1]);
-            mma_16816(o[2 * nn], pl, b[0], b[1]);
-            mma_16816(o[2 * nn + 1], ph, b[2], b[3]);
-            mma_16816(o[2 * nn + 1], pl, b[2], b[3]);
+            for (int nn = 0; nn < HD / 16; ++nn) {
+              uint32_t b[4];
+              const int mi = lane >> 3, key = kk * 16 + (mi & 1) * 8 + (lane & 7);
+              ldsm_x4_t(b, V + key * ROW + (((nn * 2 + (mi >> 1)) ^ (key & 7)) << 4));
+              mma_16816(o[2 * nn], ph[kk], b[0], b[1]);
+              mma_16816(o[2 * nn], pl[kk], b[0], b[1]);
+              mma_16816(o[2 * nn + 1], ph[kk], b[2], b[3]);
+              mma_16816(o[2 * nn + 1], pl[kk], b[2], b[3]);
+            }
+          v_half = false;
+          slot = slot + 1 == F_SLOTS ? 0 : slot + 1;
+          if (++t == w.t1) {   // the piece's result
+            const int rows = w.toks * rep, h0 = w.head * rep, tok_w = w.s.tok0 + w.tok;
+            const int worker = paged_first_worker(io, PAGED_FEW) + fw * io.ctas + blockIdx.x;
+            const PagedDest dest = paged_dest(p, io, w, worker);
+            const size_t base = paged_dest_base(p, io, dest);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              ls[i] += __shfl_xor_sync(FULL, ls[i], 1);
+              ls[i] += __shfl_xor_sync(FULL, ls[i], 2);
+              const int rr = gr + 8 * i;
+              if (rr >= rows) continue;
+              const int tok = tok_w + rr / rep, h = h0 + rr % rep;
+              const size_t row = base + paged_dest_row(io, dest, rr, tok, h);
+              if (dest.kind == PAGED_OUT) {
+                const float il = ls[i] > 0.f ? 1.f / ls[i] : 0.f;
+                bf16 *dst = (bf16 *)io.out + row * HD + tq * 2;
+#pragma unroll
+                for (int j = 0; j < HD / 8; ++j)
+                  *reinterpret_cast<__nv_bfloat162 *>(dst + j * 8) =
+                      __floats2bfloat162_rn(o[j][2 * i] * il, o[j][2 * i + 1] * il);
+              } else {
+                float *dst = io.part_o + row * HD + tq * 2;
+#pragma unroll
+                for (int j = 0; j < HD / 8; ++j)
+                  *reinterpret_cast<float2 *>(dst + j * 8) = make_float2(o[j][2 * i], o[j][2 * i + 1]);
+                if (tq == 0) {
+                  io.part_ml[row] = make_float2(m[i], ls[i]);
+                  if (dest.redirect) paged_redirect(p, io, dest, worker, tok, h);
+                }
+              }
+            }
+            w.next(p);
+            t = w.t0;
           }
-          __syncwarp();   // every lane has read the step's slots
-          issue();
         }
-        if (!ok) break;
-        const int worker = paged_first_worker(io, PAGED_FEW) + 8 * blockIdx.x + fw;
-        const PagedDest dest = paged_dest(p, io, w, worker);
-        const size_t base = paged_dest_base(p, io, dest);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          ls[i] += __shfl_xor_sync(FULL, ls[i], 1);
-          ls[i] += __shfl_xor_sync(FULL, ls[i], 2);
-          const int rr = gr + 8 * i;
-          if (rr >= rows) continue;
-          const int tok = tok_w + rr / rep, h = h0 + rr % rep;
-          const size_t row = base + paged_dest_row(io, dest, rr, tok, h);
-          if (dest.kind == PAGED_OUT) {
-            const float il = ls[i] > 0.f ? 1.f / ls[i] : 0.f;
-            bf16 *dst = (bf16 *)io.out + row * HD + tq * 2;
-#pragma unroll
-            for (int j = 0; j < HD / 8; ++j)
-              *reinterpret_cast<__nv_bfloat162 *>(dst + j * 8) =
-                  __floats2bfloat162_rn(o[j][2 * i] * il, o[j][2 * i + 1] * il);
-          } else {
-            float *dst = io.part_o + row * HD + tq * 2;
-#pragma unroll
-            for (int j = 0; j < HD / 8; ++j)
-              *reinterpret_cast<float2 *>(dst + j * 8) = make_float2(o[j][2 * i], o[j][2 * i + 1]);
-            if (tq == 0) {
-              io.part_ml[row] = make_float2(m[i], ls[i]);
-              if (dest.redirect) paged_redirect(p, io, dest, worker, tok, h);
+        __syncwarp();   // every lane has read the slot that is loaded now
+        if (lw.more()) {
+          const int pos = lw.s.key0 + lt * F_KT, pg = pos >> shift, live = lw.keys - lt * F_KT;
+          const int pg2 = (pos + 16) >> shift;   // page of the second 16 keys
+          if (lw.seg != ids_seg || pg < ids_page || pg2 >= ids_page + 32) {
+            ids_seg = lw.seg;
+            ids_page = pg;
+            ids = -1;
+            if (pg + lane <= (lw.s.key0 + lw.keys - 1) >> shift) {
+              const long long row = paged_row(io, p, lw.s.seq, 0, (pg + lane) << shift);
+              ids = row < 0 ? -1 : (int)row;
             }
           }
+          const bf16 *pool = (const bf16 *)(lv ? io.v_pages : io.k_pages);
+          uint8_t *dst = ring + ls_slot * SLOT;
+          constexpr int CPR = HD / 8, RPI = 32 / CPR;   // chunks in a row, rows a warp copies at once
+          const int c = lane % CPR, r0 = lane / CPR;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int first = __shfl_sync(FULL, ids, (g ? pg2 : pg) - ids_page);
+            const int at = first + (lw.head << shift) + ((pos + 16 * g) & ((1 << shift) - 1));
+            const bf16 *src = pool + (size_t)(first < 0 ? 0 : at) * HD + c * 8;
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; ++i) {
+              const int r = i * RPI + r0, key = 16 * g + r;
+              const bool on = first >= 0 && key < live;   // a bad page id, no key: zeros
+              cp_async16(dst + key * ROW + ((c ^ (key & 7)) << 4), on ? src + r * HD : pool, on);
+            }
+          }
+          ls_slot = ls_slot + 1 == F_SLOTS ? 0 : ls_slot + 1;
+          if (lv && ++lt == lw.t1) {
+            lw.next(p);
+            lt = lw.t0;
+          }
+          lv = !lv;
         }
+        cp_commit();   // (empty at the end, so that the count of groups in flight stays the same)
       }
-      if (!ok) {
-        if (lane == 0) p_fail(io.status, abort_flag);
-        for (uint32_t i = taken; i < issued; ++i)   // what is still in flight lands
-          (void)mbar_wait(&bar[i % F_SLOTS], (i / F_SLOTS) & 1);
-      }
+      if (!ok && lane == 0) p_fail(io.status, abort_flag);
     }
   }
   fence_before();
@@ -797,7 +809,7 @@ int run_tc(const PagedCall &c, const PagedShape &p, const PagedIO &io, cudaStrea
     return cudaFuncGetAttributes(&fa, paged_attn_tc_kernel<HD>) == cudaSuccess ? fa.numRegs : -1;
   }();
   if (regs < P_REGS) return DG_ERR_UNSUPPORTED;
-  CUtensorMap tq, tk, tv, tkf, tvf;
+  CUtensorMap tq, tk, tv;
   const uint64_t rows = (uint64_t)c.n_pages * c.Hkv * c.page_size;
   const uint32_t box = c.page_size < PAGED_TC_KT ? c.page_size : PAGED_TC_KT;
   const CUtensorMapDataType bt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -805,14 +817,11 @@ int run_tc(const PagedCall &c, const PagedShape &p, const PagedIO &io, cudaStrea
                         (uint64_t)c.Hq * HD * 2, 64, io.rep, p.qn);
   if (rc == DG_OK) rc = make_tmap_2d(&tk, bt, 2, c.k_pages, HD, rows, HD * 2, 64, box);
   if (rc == DG_OK) rc = make_tmap_2d(&tv, bt, 2, c.v_pages, HD, rows, HD * 2, 64, box);
-  if (rc == DG_OK) rc = make_tmap_2d(&tkf, bt, 2, c.k_pages, HD, rows, HD * 2, 64, F_KT);
-  if (rc == DG_OK) rc = make_tmap_2d(&tvf, bt, 2, c.v_pages, HD, rows, HD * 2, 64, F_KT);
   if (rc != DG_OK) return rc;
   note_launch(s, "paged_attn_tc");
   cudaFuncSetAttribute(paged_attn_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)C::SMEM);
-  launch_pdl(paged_attn_tc_kernel<HD>, io.ctas, P_THR, C::SMEM, s, tq, tk, tv, tkf, tvf, p,
-             io);
+  launch_pdl(paged_attn_tc_kernel<HD>, io.ctas, P_THR, C::SMEM, s, tq, tk, tv, p, io);
   return check_launch("paged_attn_tc");
 }
 

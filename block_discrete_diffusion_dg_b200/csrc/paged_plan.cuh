@@ -11,8 +11,11 @@
 // each key tile; a worker is a CTA), narrow ones (a sequence's last item if it has at most `qn` tokens:
 // one query tile; a worker is one of a CTA's two chains) and few-row ones (the last item if it has at
 // most `qf` tokens: single tokens and short tails; a worker is one of eight warps of a CTA).
-// Lengths live on the device, so each worker derives its range itself: a warp scans the sequences
-// (32 at a time) and searches the item within the sequence.
+// Lengths live on the device, so each CTA derives the ranges of its workers itself: its threads share
+// the sequences out, and a warp per worker finds its sequence in a scan over their costs, then the item
+// within it.  All costs are 32-bit: a call whose sizes could pass 2^30 is refused on the host.  (In a
+// call for a single token this stands in the way of everything else, most of it the fetching of
+// instructions, so it is kept short: 64-bit costs and a search by one thread took 11 us.)
 #pragma once
 
 #include <stdint.h>
@@ -34,7 +37,7 @@ struct PagedShape {
   int qn;                   // a last item of at most qn tokens is narrow (0: none is),
   int qf;                   // of at most qf <= qn few-row (0: none is)
   // by kind of item:
-  int kt[3];                // keys per tile
+  int kt_shift[3];          // keys per tile: 2^kt_shift
   int start_cost[3];        // cost of starting and storing an item, in key tiles
   int least[3];             // least cost worth a worker of its own
   int causal;
@@ -91,9 +94,9 @@ DG_HD PagedSeg paged_seg(const PagedShape &p, int index) {
   return s;
 }
 
-// sum_{i < n} floor((a i + b) / m) for a, b >= 0, m > 0.
-DG_HD long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long r = 0;
+// sum_{i < n} floor((a i + b) / m) for a, b >= 0, m > 0 (each term and the sum below 2^31).
+DG_HD int floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  uint32_t r = 0;
   while (n > 0) {
     if (a >= m) {
       r += (n - 1) * n / 2 * (a / m);
@@ -103,32 +106,35 @@ DG_HD long long floor_sum(long long n, long long m, long long a, long long b) {
       r += n * (b / m);
       b %= m;
     }
-    const long long y = a * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) break;
     n = y / m;
     b = y % m;
-    const long long t = m;
+    const uint32_t t = m;
     m = a;
     a = t;
   }
-  return r;
+  return (int)r;
 }
 
 enum { PAGED_WIDE = 0, PAGED_NARROW = 1, PAGED_FEW = 2 };
 
+// Full items of a segment (a division is skipped where there are none: single tokens).
+DG_HD int paged_full_items(const PagedShape &p, const PagedSeg &s) { return s.n < p.qt ? 0 : s.n / p.qt; }
 // The kind of a segment's last item where it is not wide, else PAGED_WIDE.
 DG_HD int paged_tail_kind(const PagedShape &p, const PagedSeg &s) {
-  const int tail = s.n % p.qt;
+  const int tail = s.n - paged_full_items(p, s) * p.qt;
   return tail == 0 || tail > p.qn ? PAGED_WIDE : tail > p.qf ? PAGED_NARROW : PAGED_FEW;
 }
 // Items of a kind in one kv head of segment s, and the index of the first.
 DG_HD int paged_items(const PagedShape &p, const PagedSeg &s, int kind) {
   const int tail = paged_tail_kind(p, s);
   if (kind != PAGED_WIDE) return tail == kind ? 1 : 0;
-  return tail == PAGED_WIDE ? (s.n + p.qt - 1) / p.qt : s.n / p.qt;
+  const int full = paged_full_items(p, s);
+  return full + (tail == PAGED_WIDE && full * p.qt < s.n ? 1 : 0);
 }
 DG_HD int paged_first_item(const PagedShape &p, const PagedSeg &s, int kind) {
-  return kind == PAGED_WIDE ? 0 : s.n / p.qt;
+  return kind == PAGED_WIDE ? 0 : paged_full_items(p, s);
 }
 DG_HD int paged_item_tokens(const PagedShape &p, const PagedSeg &s, int i) {
   const int left = s.n - i * p.qt;
@@ -139,109 +145,166 @@ DG_HD int paged_item_keys(const PagedShape &p, const PagedSeg &s, int i) {
   if (!s.causal) return s.keys;
   return s.keys - s.n + i * p.qt + paged_item_tokens(p, s, i);
 }
+DG_HD int paged_tiles(const PagedShape &p, int kind, int keys) {
+  return (keys + (1 << p.kt_shift[kind]) - 1) >> p.kt_shift[kind];
+}
 DG_HD int paged_item_tiles(const PagedShape &p, const PagedSeg &s, int kind, int i) {
-  return (paged_item_keys(p, s, i) + p.kt[kind] - 1) / p.kt[kind];
+  return paged_tiles(p, kind, paged_item_keys(p, s, i));
 }
 // Cost of the first q items of a kind (of one kv head).
-DG_HD long long paged_cost_before(const PagedShape &p, const PagedSeg &s, int kind, int q) {
+DG_HD int paged_cost_before(const PagedShape &p, const PagedSeg &s, int kind, int q) {
   if (q <= 0) return 0;
-  if (kind != PAGED_WIDE)
-    return paged_item_tiles(p, s, kind, paged_first_item(p, s, kind)) + p.start_cost[kind];
-  const long long start = (long long)q * p.start_cost[kind];
-  if (!s.causal) return start + (long long)q * paged_item_tiles(p, s, kind, 0);
-  // full items by their sum, the last one (which may have fewer tokens) by itself
-  const bool last = q == paged_items(p, s, kind);
-  const long long r =
-      floor_sum(last ? q - 1 : q, p.kt[kind], p.qt,
-                (long long)s.keys - s.n + p.qt + p.kt[kind] - 1);
-  return start + (last ? r + paged_item_tiles(p, s, kind, q - 1) : r);
+  // a kind other than wide has one item, which sees all of the segment's keys
+  if (kind != PAGED_WIDE || !s.causal) return q * (paged_tiles(p, kind, s.keys) + p.start_cost[kind]);
+  const int last = q * p.qt > s.n ? 1 : 0;   // an item with fewer tokens: by itself
+  const int kt = 1 << p.kt_shift[kind];
+  const int full = floor_sum(q - last, kt, p.qt, s.keys - s.n + p.qt + kt - 1);
+  return full + (last ? paged_tiles(p, kind, s.keys) : 0) + q * p.start_cost[kind];
 }
-DG_HD long long paged_head_cost(const PagedShape &p, const PagedSeg &s, int kind) {
+DG_HD int paged_head_cost(const PagedShape &p, const PagedSeg &s, int kind) {
   return s.n > 0 ? paged_cost_before(p, s, kind, paged_items(p, s, kind)) : 0;
 }
+// At least the total cost of any kind in a call of these sizes.
+inline long long paged_cost_bound(const PagedShape &p) {
+  long long most = 0;
+  for (int kind = 0; kind < 3; ++kind) {
+    const long long tiles = (p.cap >> p.kt_shift[kind]) + 1 + p.start_cost[kind];
+    const long long tails = (p.n_seqs < p.n_tokens ? p.n_seqs : p.n_tokens) + 1;
+    const long long items = kind == PAGED_WIDE ? 2 * (long long)(p.n_tokens / p.qt) + tails : tails;
+    const long long c = p.Hkv * items * tiles;
+    most = c > most ? c : most;
+  }
+  return most;
+}
+constexpr long long PAGED_COST_LIMIT = 1LL << 30;
 
 // A worker's place in the work of a kind: its range [u0, u1) of the total cost (u0 >= u1: none) and
 // the item that it begins in.
 struct PagedStart {
-  long long u0, u1;
-  long long item_u0;        // where the item that holds u0 begins
-  long long per;            // cost per worker
-  int seg, head, item;
+  int u0, u1;
+  int item_u0;              // where the item that holds u0 begins
+  int per;                  // cost per worker
+  int seg, head, item;      // item: among those of the kind
+  PagedSeg s;
 };
 
+// What a worker leaves about the item that its range goes on with, for joining the pieces.
+struct PagedHead {
+  int first, last;          // workers (of the kind) that hold its first and last tile; first < 0: the
+                            // range does not begin inside an item
+  int tok0, tokens, head;   // packed rows and kv head of the item
+  int pad[3];
+};
+DG_HD PagedHead paged_head(const PagedShape &p, int kind, const PagedStart &st) {
+  PagedHead h = {-1, 0, 0, 0, 0, {0, 0, 0}};
+  const int c = p.start_cost[kind];
+  if (st.u0 < st.u1 && st.u0 - st.item_u0 > c) {
+    const int item = paged_first_item(p, st.s, kind) + st.item;
+    const int begin = st.item_u0 + c, end = begin + paged_item_tiles(p, st.s, kind, item);
+    h.first = begin / st.per;
+    h.last = (end - 1) / st.per;
+    h.tok0 = st.s.tok0 + item * p.qt;
+    h.tokens = paged_item_tokens(p, st.s, item);
+    h.head = st.head;
+  }
+  return h;
+}
+
 #ifdef __CUDACC__
-// Called by one whole warp.  *error: the largest error code of any sequence, for the caller to
-// record.
-__device__ inline PagedStart paged_locate(const PagedShape &p, int kind, int worker, int workers,
-                                          int *error) {
-  const int lane = threadIdx.x & 31;
-  const unsigned full = 0xffffffffu;
-  const int segs = paged_segs(p);
-  long long total = 0;
-  int err = 0;
-  for (int b = 0; b < segs; b += 32) {
-    long long w = 0;
-    if (b + lane < segs) {
-      const PagedSeg s = paged_seg(p, b + lane);
-      w = p.Hkv * paged_head_cost(p, s, kind);
-      err = err > s.error ? err : s.error;
+// Workers of a kind in one CTA, and their places in the CTA's list of starts.
+constexpr int PAGED_STARTS = 11;
+__device__ __forceinline__ int paged_cta_workers(int kind) {
+  return kind == PAGED_WIDE ? 1 : kind == PAGED_NARROW ? 2 : 8;
+}
+__device__ __forceinline__ int paged_start_index(int kind) {
+  return kind == PAGED_WIDE ? 0 : kind == PAGED_NARROW ? 1 : 3;
+}
+
+struct PagedScan {
+  int before[3][256];    // by kind and thread: cost of its warp's threads before it
+  int sum[3][8];         // by kind and warp
+  int error;
+};
+
+// Finds the ranges of this CTA's workers for the kinds that have GROUP threads each (thread t works for
+// kind t / GROUP); warp j leaves the j-th worker's in start[j] and its head in heads[].  The block
+// synchronises inside, and has to before start is read.  Returns the largest error code of any sequence.
+template <int GROUP>
+__device__ __forceinline__ int paged_locate(const PagedShape &p, int cta, int ctas, int starts,
+                                            PagedStart *start, PagedHead *heads, PagedScan &scan) {
+  constexpr unsigned full = 0xffffffffu;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int segs = paged_segs(p), chunk = (segs + GROUP - 1) / GROUP;
+  if (tid == 0) scan.error = 0;
+  __syncthreads();
+  {
+    const int kind = tid / GROUP, t = tid % GROUP;
+    int mine = 0;   // cost of this thread's sequences
+    for (int i = t * chunk; i < min((t + 1) * chunk, segs); ++i) {
+      const PagedSeg s = paged_seg(p, i);
+      if (s.error) atomicMax(&scan.error, s.error);
+      mine += p.Hkv * paged_head_cost(p, s, kind);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(full, w, o);
-    total += w;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const int e = __shfl_xor_sync(full, err, o);
-    err = err > e ? err : e;
-  }
-  *error = err;
-  PagedStart r;
-  r.per = (total + workers - 1) / workers;
-  if (r.per < p.least[kind]) r.per = p.least[kind];
-  r.u0 = worker * r.per;
-  r.u1 = r.u0 + r.per < total ? r.u0 + r.per : total;
-  r.seg = r.head = r.item = 0;
-  r.item_u0 = 0;
-  if (r.u0 >= r.u1) {
-    r.u0 = r.u1 = 0;
-    return r;
-  }
-  long long before = 0;
-  for (int b = 0; b < segs; b += 32) {
-    long long w = 0;
-    if (b + lane < segs) w = p.Hkv * paged_head_cost(p, paged_seg(p, b + lane), kind);
-    long long inc = w;
+    int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(full, inc, o);
-      if (lane >= o) inc += t;
+      const int v = __shfl_up_sync(full, inc, o);
+      if (lane >= o) inc += v;
     }
-    const unsigned hit = __ballot_sync(full, before + inc > r.u0);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      r.seg = b + l;
-      before += __shfl_sync(full, inc - w, l);
-      break;
+    scan.before[kind][t] = inc - mine;
+    if (lane == 31) scan.sum[kind][t >> 5] = inc;
+  }
+  __syncthreads();
+  const int j = tid >> 5;   // this warp's worker
+  if (j < starts) {
+    const int kind = j == 0 ? PAGED_WIDE : j < 3 ? PAGED_NARROW : PAGED_FEW;
+    // workers are dealt out over the CTAs, so that a small call uses many of them
+    const int n = paged_cta_workers(kind), worker = (j - paged_start_index(kind)) * ctas + cta;
+    PagedStart r{};
+    int total = 0;
+    for (int w = 0; w < GROUP / 32; ++w) total += scan.sum[kind][w];
+    r.per = (int)((uint32_t)(total + n * ctas - 1) / (uint32_t)(n * ctas));
+    if (r.per < p.least[kind]) r.per = p.least[kind];
+    if (total > 0 && (uint32_t)worker * (uint32_t)r.per < (uint32_t)total) {
+      r.u0 = worker * r.per;
+      r.u1 = r.u0 + r.per < total ? r.u0 + r.per : total;
+      // the thread whose sequences hold u0: the last that begins at or before it
+      int w = 0, at = 0;
+      while (r.u0 >= at + scan.sum[kind][w]) at += scan.sum[kind][w++];
+      const int mine = at + scan.before[kind][w * 32 + lane];
+      const int l = 31 - __clz(__ballot_sync(full, mine <= r.u0));
+      r.item_u0 = __shfl_sync(full, mine, l);
+      int each;
+      for (r.seg = (w * 32 + l) * chunk;; ++r.seg) {
+        r.s = paged_seg(p, r.seg);
+        each = paged_head_cost(p, r.s, kind);
+        if (r.u0 < r.item_u0 + p.Hkv * each) break;
+        r.item_u0 += p.Hkv * each;
+      }
+      r.head = (r.u0 - r.item_u0) / each;
+      r.item_u0 += r.head * each;
+      // the last item that begins at or before u0: 32-way search
+      if (kind == PAGED_WIDE) {
+        int a = 0, b = paged_items(p, r.s, kind);
+#pragma unroll 1
+        while (b - a > 1) {
+          const int step = (b - a + 31) / 32, i = a + lane * step;
+          const bool le = i < b && r.item_u0 + paged_cost_before(p, r.s, kind, i) <= r.u0;
+          const int k = 31 - __clz(__ballot_sync(full, le));  // lane 0 always holds
+          a += k * step;
+          b = b < a + step ? b : a + step;
+        }
+        r.item = a;
+        r.item_u0 += paged_cost_before(p, r.s, kind, a);
+      }
     }
-    before += __shfl_sync(full, inc, 31);
+    if (lane == 0) {
+      start[j] = r;
+      heads[(kind == PAGED_WIDE ? 0 : kind == PAGED_NARROW ? ctas : 3 * ctas) + worker] =
+          paged_head(p, kind, r);
+    }
   }
-  const PagedSeg s = paged_seg(p, r.seg);
-  const long long each = paged_head_cost(p, s, kind);
-  r.head = (int)((r.u0 - before) / each);
-  before += r.head * each;
-  // the last item that begins at or before u0: 32-way search
-  int lo = 0, hi = paged_items(p, s, kind);
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
-    const bool le = i < hi && before + paged_cost_before(p, s, kind, i) <= r.u0;
-    const int l = 31 - __clz(__ballot_sync(full, le));  // lane 0 always holds
-    lo += l * step;
-    hi = hi < lo + step ? hi : lo + step;
-  }
-  r.item = lo;
-  r.item_u0 = before + paged_cost_before(p, s, kind, lo);
-  return r;
+  return scan.error;
 }
 #endif
 
@@ -254,7 +317,7 @@ struct PagedWalk {
   int item, tok, toks, keys, tiles;   // the current item; keys it visits
   int t0, t1;
   int kind;
-  long long u1, item_u0, u;
+  int u1, item_u0, u;
 
   DG_HD void begin(const PagedShape &p, int kind_, const PagedStart &st) {
     kind = kind_;
@@ -265,7 +328,7 @@ struct PagedWalk {
     u1 = st.u1;
     item_u0 = st.item_u0;
     if (u >= u1) return;
-    s = paged_seg(p, seg);
+    s = st.s;
     items = paged_items(p, s, kind);
     load(p);
     if (t0 >= t1) next(p);
@@ -277,11 +340,11 @@ struct PagedWalk {
     tok = item * p.qt;
     toks = paged_item_tokens(p, s, item);
     keys = paged_item_keys(p, s, item);
-    tiles = (keys + p.kt[kind] - 1) / p.kt[kind];
+    tiles = paged_tiles(p, kind, keys);
     const int c = p.start_cost[kind];
-    const long long a = u - item_u0 - c, b = u1 - item_u0 - c;
-    t0 = a > 0 ? (int)a : 0;
-    t1 = b < tiles ? (b > 0 ? (int)b : 0) : tiles;
+    const int a = u - item_u0 - c, b = u1 - item_u0 - c;
+    t0 = a > 0 ? a : 0;
+    t1 = b < tiles ? (b > 0 ? b : 0) : tiles;
   }
   DG_HD void next(const PagedShape &p) {
     do {
@@ -302,29 +365,5 @@ struct PagedWalk {
     } while (t0 >= t1);
   }
 };
-
-// What a worker leaves about the item that its range goes on with, for joining the pieces.
-struct PagedHead {
-  int joins;    // 1: the range begins inside an item whose first piece lies with the worker before
-  int last;     // worker (of the kind) that holds the item's last tile
-  int tok0, tokens, head;   // packed rows and kv head of the item
-  int pad[3];
-};
-DG_HD PagedHead paged_head(const PagedShape &p, int kind, const PagedStart &st) {
-  PagedHead h = {0, 0, 0, 0, 0, {0, 0, 0}};
-  const int c = p.start_cost[kind];
-  const long long in = st.u0 - st.item_u0;
-  if (st.u0 < st.u1 && in > c) {
-    const PagedSeg s = paged_seg(p, st.seg);
-    const int item = paged_first_item(p, s, kind) + st.item;
-    const long long end = st.item_u0 + c + paged_item_tiles(p, s, kind, item);
-    h.joins = in - st.per <= c;
-    h.last = (int)((end - 1) / st.per);
-    h.tok0 = s.tok0 + item * p.qt;
-    h.tokens = paged_item_tokens(p, s, item);
-    h.head = st.head;
-  }
-  return h;
-}
 
 }  // namespace dg

@@ -22,7 +22,7 @@ struct Unit { int seg, head, item, k; };
 
 // The range start as paged_locate finds it, by plain counting.
 static PagedStart locate(const PagedShape &p, int kind, int worker, int workers) {
-  long long total = 0;
+  int total = 0;
   for (int i = 0; i < paged_segs(p); ++i) total += p.Hkv * paged_head_cost(p, paged_seg(p, i), kind);
   PagedStart r{};
   r.per = (total + workers - 1) / workers;
@@ -30,13 +30,13 @@ static PagedStart locate(const PagedShape &p, int kind, int worker, int workers)
   r.u0 = worker * r.per;
   r.u1 = r.u0 + r.per < total ? r.u0 + r.per : total;
   if (r.u0 >= r.u1) { r.u0 = r.u1 = 0; return r; }
-  long long at = 0;
+  int at = 0;
   for (int i = 0; i < paged_segs(p); ++i) {
     const PagedSeg s = paged_seg(p, i);
     for (int h = 0; s.n > 0 && h < p.Hkv; ++h)
       for (int q = 0; q < paged_items(p, s, kind); ++q) {
         const int n = p.start_cost[kind] + paged_item_tiles(p, s, kind, paged_first_item(p, s, kind) + q);
-        if (r.u0 >= at && r.u0 < at + n) { r.seg = i; r.head = h; r.item = q; r.item_u0 = at; return r; }
+        if (r.u0 >= at && r.u0 < at + n) { r.seg = i; r.head = h; r.item = q; r.item_u0 = at; r.s = s; return r; }
         at += n;
       }
   }
@@ -55,8 +55,8 @@ int main() {
     const bool wide = rnd(2);
     PagedShape p{};
     p.Hkv = 1 + rnd(4);
-    p.kt[0] = p.kt[1] = wide ? 128 : 64;
-    p.kt[2] = 16;
+    p.kt_shift[0] = p.kt_shift[1] = wide ? 7 : 6;
+    p.kt_shift[2] = 5;
     for (int k = 0; k < 3; ++k) p.least[k] = rnd(2) ? rnd(9) : 0;
     p.qt = (wide ? 128 : 64) / rep * (wide ? 2 : 1);
     p.qn = wide ? 128 / rep : 0;
@@ -105,8 +105,8 @@ int main() {
         for (int q = 0; q < n; ++q) {
           CHECK(paged_cost_before(p, s, kind, q) == before);
           const int t = paged_item_tiles(p, s, kind, first + q);
-          CHECK(t > 0 && t * (long long)p.kt[kind] >= paged_item_keys(p, s, first + q));
-          CHECK((t - 1) * (long long)p.kt[kind] < paged_item_keys(p, s, first + q));
+          CHECK(t > 0 && t * (1LL << p.kt_shift[kind]) >= paged_item_keys(p, s, first + q));
+          CHECK((t - 1) * (1LL << p.kt_shift[kind]) < paged_item_keys(p, s, first + q));
           before += t + p.start_cost[kind];
         }
         CHECK(paged_cost_before(p, s, kind, n) == before && paged_head_cost(p, s, kind) == before);
@@ -115,6 +115,9 @@ int main() {
             for (int k = 0; k < paged_item_tiles(p, s, kind, first + q); ++k)
               all.push_back({i, h, first + q, k});
       }
+      long long sum = 0;
+      for (int i = 0; i < paged_segs(p); ++i) sum += p.Hkv * (long long)paged_head_cost(p, paged_seg(p, i), kind);
+      CHECK(sum <= paged_cost_bound(p));
       const int workers = rnd(2) ? 148 : 1 + rnd(300);
       size_t at = 0;
       std::vector<int> begun(workers, -1);   // the cut item that begins with a worker
@@ -136,7 +139,7 @@ int main() {
           }
           if (w.t0 > 0) {
             goes_on = true;
-            CHECK(open >= 0 && hd.joins == (open == c - 1));
+            CHECK(open >= 0 && hd.first == open);
             CHECK(hd.tok0 == w.s.tok0 + w.tok && hd.tokens == w.toks && hd.head == w.head);
             if (open_last < 0) open_last = hd.last;
             CHECK(open_last == hd.last);
@@ -149,7 +152,7 @@ int main() {
           ++pieces;
         }
         (void)open_tiles;
-        if (!goes_on) CHECK(hd.joins == 0);
+        CHECK((hd.first >= 0) == goes_on);
         CHECK(slots[0] <= 1 && slots[1] <= 1);
       }
       CHECK(at == all.size() && open < 0);
@@ -158,7 +161,7 @@ int main() {
   // error codes
   int off[] = {0, 4, 2, 9, 12, 12}, kv[] = {5, 5, -1, 97, 1000000};
   PagedShape p{};
-  p.seq_off = off; p.kv_len = kv; p.n_seqs = 5; p.n_tokens = 12; p.Hkv = 1; p.qt = 64; p.kt[0] = 64; p.cap = 99;
+  p.seq_off = off; p.kv_len = kv; p.n_seqs = 5; p.n_tokens = 12; p.Hkv = 1; p.qt = 64; p.kt_shift[0] = 6; p.cap = 99;
   CHECK(paged_seg(p, 0).error == 0 && paged_seg(p, 0).n == 4 && paged_seg(p, 0).keys == 9);
   CHECK(paged_seg(p, 1).error == 1 && paged_seg(p, 1).n == 0);       // descending offsets
   CHECK(paged_seg(p, 2).error == 1 && paged_seg(p, 2).n == 0);       // negative length
