@@ -133,7 +133,9 @@ int dg_qk_norm_rope(const dg_config *cfg, int batch, int n_tokens, const void *q
                     int32_t *dev_status, void *stream) {
   const NvtxRange nvtx_range("dg_qk_norm_rope");
   if (!cfg_ok(cfg) || batch <= 0 || n_tokens <= 0) return DG_ERR_INVALID_ARG;
-  if (!qkv_ok(cfg, qkv, ld_qkv, (long long)batch * n_tokens)) return DG_ERR_INVALID_ARG;
+  if (!qkv_ok(cfg, qkv, ld_qkv, (long long)batch * n_tokens) || !aligned16(q_gain) ||
+      !aligned16(k_gain))
+    return DG_ERR_INVALID_ARG;
   if (!cache_len || !q || !k_new || !v_new || !aligned16(q) || !aligned16(k_new) ||
       !aligned16(v_new))
     return DG_ERR_INVALID_ARG;
@@ -155,7 +157,8 @@ int dg_paged_append(const dg_config *cfg, int n_seqs, int n_tokens, const int32_
                     int32_t *dev_status, void *stream) {
   const NvtxRange nvtx_range("dg_paged_append");
   if (!sizes_ok(cfg, n_seqs, n_tokens) || !pages_ok(cfg, kv)) return DG_ERR_INVALID_ARG;
-  if (!qkv_ok(cfg, qkv, ld_qkv, n_tokens)) return DG_ERR_INVALID_ARG;
+  if (!qkv_ok(cfg, qkv, ld_qkv, n_tokens) || !aligned16(q_gain) || !aligned16(k_gain))
+    return DG_ERR_INVALID_ARG;
   if (!seq_off || !kv_len || (q && !aligned16(q))) return DG_ERR_INVALID_ARG;
   QkvCall c = qkv_call(cfg, qkv, ld_qkv, q_gain, k_gain, dev_status);
   if (!rope_spec(cfg, rope, &c.rope)) return DG_ERR_INVALID_ARG;

@@ -21,19 +21,21 @@
 
 #include "dg_common.cuh"
 #include "dg_kernels.h"
+#include "tc_host.h"
 
 namespace dg {
 
 namespace {
 
 constexpr int Q_THR = 256;
-constexpr int Q_TOK = 8;         // tokens per block
+constexpr int Q_TOK = 8;         // tokens per block at most
 constexpr int Q_MAX_PAIRS = 64;  // head_dim <= 128
 
 struct QkvArgs {
   const void *qkv;
   long long ld;                  // elements between rows
   int n_tokens, n_seqs, n;       // n > 0: uniform rows per sequence (seq_off unused)
+  int block_tokens;              // tokens per block
   const int32_t *seq_off, *len;
   int Hq, Hkv, rot, interleaved;
   float eps, mscale;
@@ -94,6 +96,43 @@ struct TokenSpot {
   long long kv_row;      // K/V row of kv head 0 (in rows of hd), -1: not written
 };
 
+// Where packed row t goes, found by one whole warp (32 sequences at a time).
+__device__ __forceinline__ TokenSpot packed_spot(const QkvArgs &a, int t, int *pos_out) {
+  const int lane = threadIdx.x & 31;
+  TokenSpot sp{-1, -1};
+  // last sequence that begins at or before row t: 32-way search
+  int lo = 0, hi = a.n_seqs;
+#pragma unroll 1
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const bool le = i < hi && (i == lo || a.seq_off[i] <= t);
+    const int l = 31 - __clz(__ballot_sync(0xffffffffu, le));
+    lo += l * step;
+    hi = min(hi, lo + step);
+  }
+  const int o0 = a.seq_off[lo], o1 = a.seq_off[lo + 1], have = a.len[lo];
+  if (o0 > t || t >= o1) return sp;   // no sequence's row
+  if (o0 < 0 || o1 > a.n_tokens || have < 0) {
+    if (lane == 0) set_status(a.status, DG_ERR_INVALID_ARG);
+    return sp;
+  }
+  sp.row = t;
+  // (a position past 2^31 is past every cache: its q is rotated by the wrapped position)
+  const int pos = (int)((uint32_t)have + (uint32_t)(t - o0));
+  *pos_out = pos;
+  if ((long long)have + (o1 - o0) > ((long long)a.max_pages << a.page_shift)) {
+    if (lane == 0) set_status(a.status, DG_ERR_CAPACITY);
+    return sp;
+  }
+  const int id = a.page_table[(size_t)lo * a.max_pages + (pos >> a.page_shift)];
+  if ((unsigned)id >= (unsigned)a.n_pages) {
+    if (lane == 0) set_status(a.status, DG_ERR_INVALID_ARG);
+    return sp;
+  }
+  sp.kv_row = (((long long)id * a.Hkv) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+  return sp;
+}
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(Q_THR) qkv_rows_kernel(const __grid_constant__ QkvArgs a) {
   pdl_wait();
@@ -104,71 +143,8 @@ __global__ void __launch_bounds__(Q_THR) qkv_rows_kernel(const __grid_constant__
   __shared__ int pos_s[Q_TOK];
   // (c, s) of the 8 pairs of lane l: two pairs per float4, entry [token][pair couple][lane]
   __shared__ float4 cs[Q_TOK][4][LPH];
-  const int tid = threadIdx.x, t0 = blockIdx.x * Q_TOK;
+  const int tid = threadIdx.x, t0 = blockIdx.x * a.block_tokens;
   const int head_stride = a.n > 0 ? a.n : 1 << a.page_shift;   // K/V rows between kv heads
-
-  if (tid < Q_TOK) {
-    TokenSpot sp{-1, -1};
-    int pos = 0;
-    const int t = t0 + tid;
-    if (t < a.n_tokens) {
-      if (a.n > 0) {
-        const int b = t / a.n, i = t % a.n;
-        sp.row = t;
-        sp.kv_row = (long long)b * a.Hkv * a.n + i;
-        pos = a.len[b] + i;
-      } else {
-        int lo = 0, hi = a.n_seqs;             // last sequence that begins at or before row t
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) / 2;
-          if (a.seq_off[mid] <= t) lo = mid;
-          else hi = mid;
-        }
-        const int o0 = a.seq_off[lo], o1 = a.seq_off[lo + 1], have = a.len[lo];
-        if (o0 <= t && t < o1) {
-          const long long cap = (long long)a.max_pages << a.page_shift;
-          if (o0 < 0 || o1 > a.n_tokens || have < 0) {
-            set_status(a.status, DG_ERR_INVALID_ARG);
-          } else {
-            sp.row = t;
-            pos = have + (t - o0);
-            if ((long long)have + (o1 - o0) > cap) {
-              set_status(a.status, DG_ERR_CAPACITY);
-            } else {
-              const int id = a.page_table[(size_t)lo * a.max_pages + (pos >> a.page_shift)];
-              if ((unsigned)id >= (unsigned)a.n_pages)
-                set_status(a.status, DG_ERR_INVALID_ARG);
-              else
-                sp.kv_row = (((long long)id * a.Hkv) << a.page_shift) +
-                            (pos & ((1 << a.page_shift) - 1));
-            }
-          }
-        }
-      }
-    }
-    spot[tid] = sp;
-    pos_s[tid] = pos;
-  }
-  __syncthreads();
-  for (int e = tid; e < Q_TOK * (a.rot / 2); e += Q_THR) {
-    const int tk = e / (a.rot / 2), x = e % (a.rot / 2), lane = x / 8, u = x % 8;
-    if (spot[tk].row < 0) continue;
-    // pair u of rotated lane `lane` (see the chunk choice below)
-    const int j = !a.interleaved ? 8 * lane + u
-                  : u < 4        ? 4 * lane + u
-                                 : 4 * (lane + a.rot / 16) + u - 4;
-    const double turns = (double)pos_s[tk] * a.turn[j];
-    const double r = turns - rint(turns);
-    const float rf = (float)r;
-    const float d = (float)(r - (double)rf) * 6.283185307179586f;
-    float sn, co;
-    sincospif(2.f * rf, &sn, &co);
-    float *o = reinterpret_cast<float *>(&cs[tk][u >> 1][lane]) + 2 * (u & 1);
-    o[0] = (co - sn * d) * a.mscale;
-    o[1] = (sn + co * d) * a.mscale;
-  }
-  __syncthreads();
-
   const int l = tid % LPH, slot = tid / LPH;
   const int heads = a.Hq + 2 * a.Hkv;
   // The lane's two chunks of 8 elements: in the rotated part chunk l and its partner half a
@@ -176,15 +152,70 @@ __global__ void __launch_bounds__(Q_THR) qkv_rows_kernel(const __grid_constant__
   const int rl = a.rot / 16;
   const int ca = l < rl ? l : 2 * rl + 2 * (l - rl);
   const int cb = l < rl ? l + rl : ca + 1;
-  const int toks = min(Q_TOK, a.n_tokens - t0);
-  for (int w = slot; w < toks * heads; w += SLOTS) {
-    const int tk = w / heads, h = w % heads;
-    const TokenSpot sp = spot[tk];
-    const bool on = sp.row >= 0;
-    const T *src = (const T *)a.qkv + (size_t)(on ? sp.row : t0) * a.ld + (size_t)h * HD;
-    Chunk<T> A, B;
+  const int toks = min(a.block_tokens, a.n_tokens - t0), work = toks * heads;
+  // The rows are read a step ahead: their place does not depend on the sequences, so the first
+  // are under way while those are searched and the angles computed.
+  Chunk<T> A, B;
+  int tk = slot / heads, h = slot % heads;
+  const T *src = (const T *)a.qkv + (size_t)(t0 + tk) * a.ld + (size_t)h * HD;
+  if (slot < work) {
     A.load(src + ca * 8);
     B.load(src + cb * 8);
+  }
+  {
+    const int w = tid >> 5;   // a warp per token
+    if (w < toks) {
+      const int t = t0 + w;
+      TokenSpot sp;
+      int pos = 0;
+      if (a.n > 0) {
+        const int b = t / a.n, i = t % a.n;
+        sp.row = t;
+        sp.kv_row = (long long)b * a.Hkv * a.n + i;
+        pos = a.len[b] + i;
+      } else {
+        sp = packed_spot(a, t, &pos);
+      }
+      if ((tid & 31) == 0) {
+        spot[w] = sp;
+        pos_s[w] = pos;
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int e = tid; e < toks * (a.rot / 2); e += Q_THR) {
+    const int k = e / (a.rot / 2), x = e % (a.rot / 2), lane = x / 8, u = x % 8;
+    // pair u of rotated lane `lane`
+    const int j = !a.interleaved ? 8 * lane + u
+                  : u < 4        ? 4 * lane + u
+                                 : 4 * (lane + rl) + u - 4;
+    const double turns = (double)pos_s[k] * a.turn[j];
+    const double r = turns - rint(turns);
+    const float rf = (float)r;
+    const float d = (float)(r - (double)rf) * 6.283185307179586f;
+    float sn, co;
+    sincospif(2.f * rf, &sn, &co);
+    float *o = reinterpret_cast<float *>(&cs[k][u >> 1][lane]) + 2 * (u & 1);
+    o[0] = (co - sn * d) * a.mscale;
+    o[1] = (sn + co * d) * a.mscale;
+  }
+  __syncthreads();
+
+#pragma unroll 1
+  for (int w = slot; w < work; w += SLOTS) {
+    Chunk<T> A2, B2;
+    int h2 = h + SLOTS, tk2 = tk;
+    while (h2 >= heads) {
+      h2 -= heads;
+      ++tk2;
+    }
+    if (w + SLOTS < work) {
+      src = (const T *)a.qkv + (size_t)(t0 + tk2) * a.ld + (size_t)h2 * HD;
+      A2.load(src + ca * 8);
+      B2.load(src + cb * 8);
+    }
+    const TokenSpot sp = spot[tk];
     const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
     const float *gain = is_q ? a.q_gain : is_v ? nullptr : a.k_gain;
     if (!is_v) {
@@ -200,11 +231,16 @@ __global__ void __launch_bounds__(Q_THR) qkv_rows_kernel(const __grid_constant__
 #pragma unroll
         for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
         const float rs = 1.f / sqrtf(ss * (1.f / HD) + a.eps);
+        Chunk<float> ga, gb;
+        float g[8];
+        ga.load(gain + ca * 8);
+        gb.load(gain + cb * 8);
+        ga.get(g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] *= rs * gain[ca * 8 + i];
-          y[i] *= rs * gain[cb * 8 + i];
-        }
+        for (int i = 0; i < 8; ++i) x[i] *= rs * g[i];
+        gb.get(g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= rs * g[i];
       }
       if (l < rl) {
 #pragma unroll
@@ -229,19 +265,22 @@ __global__ void __launch_bounds__(Q_THR) qkv_rows_kernel(const __grid_constant__
       A.set(x);
       B.set(y);
     }
-    if (!on) continue;
-    T *dst;
+    T *dst = nullptr;
     if (is_q) {
-      dst = a.q ? (T *)a.q + ((size_t)sp.row * a.Hq + h) * HD : nullptr;
-    } else {
+      if (sp.row >= 0 && a.q) dst = (T *)a.q + ((size_t)sp.row * a.Hq + h) * HD;
+    } else if (sp.kv_row >= 0) {
       const int g = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
       T *base = (T *)(a.n > 0 ? (is_v ? a.v : a.k) : (is_v ? a.v_pages : a.k_pages));
-      dst = sp.kv_row < 0 ? nullptr : base + (sp.kv_row + (long long)g * head_stride) * HD;
+      dst = base + (sp.kv_row + (long long)g * head_stride) * HD;
     }
     if (dst) {
       A.store(dst + ca * 8);
       B.store(dst + cb * 8);
     }
+    A = A2;
+    B = B2;
+    h = h2;
+    tk = tk2;
   }
 }
 
@@ -298,7 +337,11 @@ int launch_qkv_rows(const QkvCall &c, cudaStream_t s) {
   while ((1 << a.page_shift) < c.page_size) ++a.page_shift;
   a.status = c.status;
   fill_turns(c.rope, a.turn);
-  const int grid = (c.n_tokens + Q_TOK - 1) / Q_TOK;
+  // few tokens: a block each, so that every head of a call for single tokens is in flight at once
+  const int spread = 4 * num_sms();
+  a.block_tokens = (c.n_tokens + spread - 1) / spread;
+  if (a.block_tokens > Q_TOK) a.block_tokens = Q_TOK;
+  const int grid = (c.n_tokens + a.block_tokens - 1) / a.block_tokens;
   note_launch(s, "qkv_rows");
 #define DG_QKV_CASE(T, HD) launch_pdl(qkv_rows_kernel<T, HD>, grid, Q_THR, 0, s, a)
   if (c.act == DG_F32) {
