@@ -28,7 +28,7 @@ namespace dg {
 namespace {
 
 constexpr int Q_THR = 256;
-constexpr int Q_TOK = 8;         // tokens per block at most
+constexpr int Q_TOK = 16;        // tokens per block at most
 constexpr int Q_MAX_PAIRS = 64;  // head_dim <= 128
 
 struct QkvArgs {
@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(Q_THR) qkv_rows_kernel(const __grid_constant__
     B.load(src + cb * 8);
   }
   {
-    const int w = tid >> 5;   // a warp per token
-    if (w < toks) {
+    // a warp per token
+#pragma unroll 1
+    for (int w = tid >> 5; w < toks; w += Q_THR / 32) {
       const int t = t0 + w;
       TokenSpot sp;
       int pos = 0;
@@ -338,9 +339,9 @@ int launch_qkv_rows(const QkvCall &c, cudaStream_t s) {
   a.status = c.status;
   fill_turns(c.rope, a.turn);
   // few tokens: a block each, so that every head of a call for single tokens is in flight at once
-  const int spread = 4 * num_sms();
-  a.block_tokens = (c.n_tokens + spread - 1) / spread;
-  if (a.block_tokens > Q_TOK) a.block_tokens = Q_TOK;
+  // (four blocks fit an SM); many: whole waves of blocks
+  const int spread = 4 * num_sms(), waves = (c.n_tokens - 1) / (spread * Q_TOK) + 1;
+  a.block_tokens = (c.n_tokens - 1) / (spread * waves) + 1;
   const int grid = (c.n_tokens + a.block_tokens - 1) / a.block_tokens;
   note_launch(s, "qkv_rows");
 #define DG_QKV_CASE(T, HD) launch_pdl(qkv_rows_kernel<T, HD>, grid, Q_THR, 0, s, a)
