@@ -399,6 +399,8 @@ class PagedKV:
         if page_table.dim() != 2 or page_table.dtype != torch.int32:
             raise ValueError("the page table is int32 [n_seqs][max_pages]")
         self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
+        self.act, self.kv_heads, self.head_dim = k_pages.dtype, k_pages.shape[1], k_pages.shape[3]
+        self.seqs = page_table.shape[0]
         self.struct = DgPagedKv(_p(k_pages), _p(v_pages), _p(page_table), k_pages.shape[0],
                                 k_pages.shape[2], page_table.shape[1])
         self.ref = ctypes.byref(self.struct)
@@ -430,10 +432,9 @@ def _gain(cfg, g, name):
 
 
 def _pages(cfg, kv: PagedKV, n_seqs):
-    k = kv.k_pages
-    if k.dtype != _ACT[cfg.act_dtype] or k.shape[1] != cfg.n_kv_heads or k.shape[3] != cfg.head_dim:
+    if kv.act != _ACT[cfg.act_dtype] or kv.kv_heads != cfg.n_kv_heads or kv.head_dim != cfg.head_dim:
         raise ValueError("the pages do not fit the config")
-    if kv.page_table.shape[0] < n_seqs:
+    if kv.seqs < n_seqs:
         raise ValueError("the page table has fewer rows than there are sequences")
     return kv.ref
 
@@ -444,14 +445,25 @@ def _index(t, name, n):
     return _p(t)
 
 
-def _launch(fn, what, device, stream, *args):
-    """fn(*args, stream) on the tensors' device, which need not be the current one."""
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(stream))
+# The two lookups of a launch without the Python layers above them (4 us of a 14 us call).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(name, device, stream, *args):
+    """The library's `name`(*args, stream) on the tensors' device, which need not be the current
+    one; stream None: that device's current stream."""
+    fn = getattr(_lib or lib(), name)
+    index = device.index
+    s = _raw_stream(index) if stream is None else _stream(stream)
+    if index == _current_device():
+        rc = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, _stream(stream))
-    _check(rc, what)
+            rc = fn(*args, s)
+    if rc != DG_OK:
+        raise DgError(rc, name)
 
 
 def dg_qk_norm_rope(cfg, batch, n_tokens, qkv, cache_len, q_gain, k_gain, rope: Optional[DgRope], q,
@@ -459,7 +471,7 @@ def dg_qk_norm_rope(cfg, batch, n_tokens, qkv, cache_len, q_gain, k_gain, rope: 
     """Per-head norms, rotation and head split of projected rows (ready for dg_canvas_attn)."""
     ptr, ld = _qkv_rows(cfg, qkv, batch * n_tokens)
     act, hd, hkv = _ACT[cfg.act_dtype], cfg.head_dim, cfg.n_kv_heads
-    _launch(lib().dg_qk_norm_rope, "dg_qk_norm_rope", qkv.device, stream, ctypes.byref(cfg), batch,
+    _launch("dg_qk_norm_rope", qkv.device, stream, ctypes.byref(cfg), batch,
             n_tokens, ptr, ld, _index(cache_len, "cache_len", batch), _gain(cfg, q_gain, "q_gain"),
             _gain(cfg, k_gain, "k_gain"), None if rope is None else ctypes.byref(rope),
             _rows(q, "q", act, batch, n_tokens, cfg.n_q_heads, hd),
@@ -471,7 +483,7 @@ def dg_paged_append(cfg, n_seqs, n_tokens, seq_off, kv_len, qkv, q_gain, k_gain,
                     rope: Optional[DgRope], kv: PagedKV, q, dev_status=None, stream=None):
     """Per-head norms and rotation of packed rows; q packed, K and V into their pages."""
     ptr, ld = _qkv_rows(cfg, qkv, n_tokens)
-    _launch(lib().dg_paged_append, "dg_paged_append", qkv.device, stream, ctypes.byref(cfg), n_seqs,
+    _launch("dg_paged_append", qkv.device, stream, ctypes.byref(cfg), n_seqs,
             n_tokens, _index(seq_off, "seq_off", n_seqs + 1), _index(kv_len, "kv_len", n_seqs), ptr,
             ld, _gain(cfg, q_gain, "q_gain"), _gain(cfg, k_gain, "k_gain"),
             None if rope is None else ctypes.byref(rope), _pages(cfg, kv, n_seqs),
@@ -495,7 +507,7 @@ def dg_paged_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, q, kv: PagedKV, causal
     """Attention of packed sequences over their pages (the new K and V already appended)."""
     w, wb = _ws(ws)
     act, hq, hd = _ACT[cfg.act_dtype], cfg.n_q_heads, cfg.head_dim
-    _launch(lib().dg_paged_attn, "dg_paged_attn", q.device, stream, ctypes.byref(cfg), n_seqs,
+    _launch("dg_paged_attn", q.device, stream, ctypes.byref(cfg), n_seqs,
             n_tokens, _index(seq_off, "seq_off", n_seqs + 1), _index(kv_len, "kv_len", n_seqs),
             _rows(q, "q", act, n_tokens, hq, hd), _pages(cfg, kv, n_seqs), 1 if causal else 0,
             _rows(out, "out", act, n_tokens, hq, hd), w, wb, _p(dev_status))
@@ -506,7 +518,7 @@ def dg_prefix_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, shared_len, q, kv: Pa
     """dg_paged_attn where the first shared_len keys are common to all sequences, read once."""
     w, wb = _ws(ws)
     act, hq, hd = _ACT[cfg.act_dtype], cfg.n_q_heads, cfg.head_dim
-    _launch(lib().dg_prefix_attn, "dg_prefix_attn", q.device, stream, ctypes.byref(cfg), n_seqs,
+    _launch("dg_prefix_attn", q.device, stream, ctypes.byref(cfg), n_seqs,
             n_tokens, _index(seq_off, "seq_off", n_seqs + 1), _index(kv_len, "kv_len", n_seqs),
             shared_len, _rows(q, "q", act, n_tokens, hq, hd), _pages(cfg, kv, n_seqs),
             1 if causal else 0, _rows(out, "out", act, n_tokens, hq, hd), w, wb, _p(dev_status))
