@@ -66,6 +66,12 @@ struct Tc {
   static constexpr size_t SMEM = 1024 + (size_t)TILE * (2 + STAGES) + 8 * P_STAGE + 2048;
 };
 
+// A piece of a few-row item, as the loading side of a warp leaves it for the computing side.
+struct FewPiece {
+  int tok, toks, head, keys, before, t0, t1, which;
+  bool whole;
+};
+
 template <int R>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(P_THR, 1)
       ++fill;
     };
     // Tiles are loaded in the order in which the MMA warp releases them.
-    {
+    if (start[0].u1 > 0) {
       PagedWalk w;
       for (w.begin(p, PAGED_WIDE, start[0]); ok && w.more(); w.next(p)) {
         load_q(w, 0, w.tok);
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(P_THR, 1)
         }
       }
     }
-    {
+    if (start[1].u1 > 0 || start[2].u1 > 0) {
       PagedWalk w[2];
       int t[2] = {0, 0}, y[2] = {0, 0};
       auto load_k = [&](int x) {
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(P_THR, 1)
       ++pieces[x];
     };
     uint32_t f = 0;   // fills taken so far (wide: the key tile whose S is issued next)
-    {
+    if (start[0].u1 > 0) {
       PagedWalk w;
       for (w.begin(p, PAGED_WIDE, start[0]); ok && w.more(); w.next(p)) {
         begin_q(0);
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(P_THR, 1)
         }
       }
     }
-    {
+    if (start[1].u1 > 0 || start[2].u1 > 0) {
       PagedWalk w[2];
       int t[2] = {0, 0};
       auto next_s = [&](int x) {
@@ -435,6 +441,7 @@ __global__ void __launch_bounds__(P_THR, 1)
     uint32_t ns = 0;                          // key tiles of this chain so far
     bool ok = true;
     for (int kind = 0; kind < 2 && ok; ++kind) {
+      if (start[kind == PAGED_WIDE ? 0 : 1 + x].u1 == 0) continue;
       PagedWalk w;
       for (w.begin(p, kind, start[kind == PAGED_WIDE ? 0 : 1 + x]); w.more(); w.next(p)) {
         const int tile0 = kind == PAGED_WIDE ? x * qn : 0;        // first token of the chain's tile
@@ -596,13 +603,15 @@ __global__ void __launch_bounds__(P_THR, 1)
       // Copies run F_SLOTS slots ahead of the arithmetic, across items: slot n of the walk is K (n even)
       // or V of a step, one group of cp.async each.  Rows behind the last key are filled with zeros.
       // Each lane holds the first row (for kv head 0) of a page, 32 pages of a sequence at a time.
-      PagedWalk lw, w;
-      lw.begin(p, PAGED_FEW, few_start);
+      // The loading side walks the items and leaves each piece's description for the computing side.
+      PagedFewWalk lw;
+      lw.begin(p, few_start);
       int lt = lw.t0, ids = 0, ids_seg = -1, ids_page = 0;
       bool lv = false;
       uint32_t ls_slot = 0, slot = 0;                           // slots loaded and used next
-      w.begin(p, PAGED_FEW, few_start);
-      int t = w.t0, lead = F_SLOTS;
+      FewPiece *pieces = reinterpret_cast<FewPiece *>(stage);   // [4], this warp's
+      uint32_t lp = 0, np = 0;                                  // pieces described and computed
+      int t = 0, t1 = 0, lead = F_SLOTS;
       bool v_half = false;
       int seen[2] = {0, 0};                                     // keys that rows gr and gr + 8 see
       uint32_t qf[HD / 16][4], ph[2][4], pl[2][4];
@@ -611,26 +620,27 @@ __global__ void __launch_bounds__(P_THR, 1)
         if (lead > 0) {
           --lead;
         } else if (!v_half) {
-          if (!w.more()) break;
-          const int rows = w.toks * rep, h0 = w.head * rep, tok_w = w.s.tok0 + w.tok;
-          if (t == w.t0) {   // an item's piece begins: Q as the A operand, rows gr and gr + 8
-            const bf16 *q0 =
-                (const bf16 *)io.q + ((size_t)(tok_w + gr / rep) * io.Hq + h0 + gr % rep) * HD + tq * 2;
-            const bf16 *q1 = (const bf16 *)io.q +
-                             ((size_t)(tok_w + (gr + 8) / rep) * io.Hq + h0 + (gr + 8) % rep) * HD + tq * 2;
+          if (t == t1) {   // the next piece: Q as the A operand, rows gr and gr + 8
+            if (np == lp) break;
+            const FewPiece pc = pieces[np & 3];
+            const int rows = pc.toks * rep, h0 = pc.head * rep;
+            t = pc.t0;
+            t1 = pc.t1;
+            // (rows past the last repeat it and are not stored)
+            const bf16 *q[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int rr = min(gr + 8 * i, rows - 1), tl = rr / rep;
+              q[i] = (const bf16 *)io.q + ((size_t)(pc.tok + tl) * io.Hq + h0 + rr - tl * rep) * HD + tq * 2;
+              seen[i] = pc.before < 0 ? pc.keys : pc.before + tl + 1;
+              m[i] = -INFINITY;
+              ls[i] = 0.f;
+            }
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                qf[kk][i] = gr + 8 * (i & 1) < rows ? *reinterpret_cast<const uint32_t *>(
-                                                          (i & 1 ? q1 : q0) + kk * 16 + (i >> 1) * 8)
-                                                    : 0u;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              seen[i] = w.s.causal ? w.s.keys - w.s.n + w.tok + min(gr + 8 * i, rows - 1) / rep + 1 : w.keys;
-              m[i] = -INFINITY;
-              ls[i] = 0.f;
-            }
+                qf[kk][i] = *reinterpret_cast<const uint32_t *>(q[i & 1] + kk * 16 + (i >> 1) * 8);
 #pragma unroll
             for (int j = 0; j < HD / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
           }
@@ -715,18 +725,20 @@ __global__ void __launch_bounds__(P_THR, 1)
             }
           v_half = false;
           slot = slot + 1 == F_SLOTS ? 0 : slot + 1;
-          if (++t == w.t1) {   // the piece's result
-            const int rows = w.toks * rep, h0 = w.head * rep, tok_w = w.s.tok0 + w.tok;
+          if (++t == t1) {   // the piece's result
+            const FewPiece pc = pieces[np & 3];
+            const int rows = pc.toks * rep, h0 = pc.head * rep;
             const int worker = paged_first_worker(io, PAGED_FEW) + fw * io.ctas + blockIdx.x;
-            const PagedDest dest = paged_dest(p, io, w, worker);
+            const PagedDest dest = paged_dest(p, io, pc.which, pc.t0 == 0, pc.whole, worker);
             const size_t base = paged_dest_base(p, io, dest);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+              if (8 * i >= rows) break;
               ls[i] += __shfl_xor_sync(FULL, ls[i], 1);
               ls[i] += __shfl_xor_sync(FULL, ls[i], 2);
               const int rr = gr + 8 * i;
               if (rr >= rows) continue;
-              const int tok = tok_w + rr / rep, h = h0 + rr % rep;
+              const int tok = pc.tok + rr / rep, h = h0 + rr % rep;
               const size_t row = base + paged_dest_row(io, dest, rr, tok, h);
               if (dest.kind == PAGED_OUT) {
                 const float il = ls[i] > 0.f ? 1.f / ls[i] : 0.f;
@@ -746,20 +758,25 @@ __global__ void __launch_bounds__(P_THR, 1)
                 }
               }
             }
-            w.next(p);
-            t = w.t0;
+            ++np;
           }
         }
         __syncwarp();   // every lane has read the slot that is loaded now
         if (lw.more()) {
-          const int pos = lw.s.key0 + lt * F_KT, pg = pos >> shift, live = lw.keys - lt * F_KT;
+          if (!lv && lt == lw.t0) {   // a piece begins: at most three are described and not yet done
+            if (lane == 0)
+              pieces[lp & 3] = FewPiece{lw.tok, lw.toks, lw.head, lw.keys, lw.before, lw.t0, lw.t1,
+                                        lw.which, lw.whole()};
+            ++lp;
+          }
+          const int pos = lw.key0 + lt * F_KT, pg = pos >> shift, live = lw.keys - lt * F_KT;
           const int pg2 = (pos + 16) >> shift;   // page of the second 16 keys
           if (lw.seg != ids_seg || pg < ids_page || pg2 >= ids_page + 32) {
             ids_seg = lw.seg;
             ids_page = pg;
             ids = -1;
-            if (pg + lane <= (lw.s.key0 + lw.keys - 1) >> shift) {
-              const long long row = paged_row(io, p, lw.s.seq, 0, (pg + lane) << shift);
+            if (pg + lane <= (lw.key0 + lw.keys - 1) >> shift) {
+              const long long row = paged_row(io, p, lw.seq, 0, (pg + lane) << shift);
               ids = row < 0 ? -1 : (int)row;
             }
           }

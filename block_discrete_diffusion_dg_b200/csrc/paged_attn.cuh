@@ -83,17 +83,21 @@ __device__ __forceinline__ size_t paged_region_row(const PagedShape &p, const Pa
   return io.region + ((size_t)which * p.n_tokens + tok) * io.Hq + h;
 }
 
-// Where the current piece of a walk goes: a whole item to the output (or its half of the region),
-// a part of one to a slot of this worker (slot 1 if the item begins here, slot 0 if it goes on from
-// an earlier worker; a range holds at most one of each).
+// Where a piece goes: a whole item to the output (or its half of the region), a part of one to a slot
+// of this worker (slot 1 if the item begins here, slot 0 if it goes on from an earlier worker; a range
+// holds at most one of each).
+__device__ __forceinline__ PagedDest paged_dest(const PagedShape &p, const PagedIO &io, int which,
+                                                bool begins, bool whole, int worker) {
+  PagedDest d;
+  d.which = which;
+  d.kind = !whole ? PAGED_SLOT : p.shared_len > 0 ? PAGED_REGION : PAGED_OUT;
+  d.slot = paged_slot_row(io, worker, begins, 0);
+  d.redirect = d.kind == PAGED_SLOT && begins && p.shared_len > 0;
+  return d;
+}
 __device__ __forceinline__ PagedDest paged_dest(const PagedShape &p, const PagedIO &io,
                                                 const PagedWalk &w, int worker) {
-  PagedDest d;
-  d.which = p.shared_len > 0 && w.seg == 0 ? 0 : 1;
-  d.kind = !w.whole() ? PAGED_SLOT : p.shared_len > 0 ? PAGED_REGION : PAGED_OUT;
-  d.slot = paged_slot_row(io, worker, w.t0 == 0, 0);
-  d.redirect = d.kind == PAGED_SLOT && w.t0 == 0 && p.shared_len > 0;
-  return d;
+  return paged_dest(p, io, p.shared_len > 0 && w.seg == 0 ? 0 : 1, w.t0 == 0, w.whole(), worker);
 }
 // Row of the destination that holds packed row (tok, h), row r of the item, without the base.
 __device__ __forceinline__ size_t paged_dest_base(const PagedShape &p, const PagedIO &io,

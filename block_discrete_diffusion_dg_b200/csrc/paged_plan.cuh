@@ -366,4 +366,58 @@ struct PagedWalk {
   }
 };
 
+// The walk of few-row items alone: a segment has at most one, the same for every kv head, so that going
+// on costs a few operations and, at the end of a sequence's heads, the lengths of the next.
+struct PagedFewWalk {
+  int seq, head, seg, which;          // which: 0 the shared prefix, 1 the sequence's own keys
+  int tok, toks;                      // packed rows [tok, tok + toks)
+  int key0, keys, tiles;              // keys [key0, key0 + keys)
+  int before;                         // keys that the first of the rows sees besides itself; < 0: all
+  int t0, t1, left;                   // tiles of this piece; cost left in the range from its item on
+
+  DG_HD bool more() const { return t0 < t1; }
+  DG_HD bool whole() const { return t0 == 0 && t1 == tiles; }
+  DG_HD void take(const PagedShape &p, const PagedSeg &s) {
+    const int first = paged_full_items(p, s) * p.qt;
+    seq = s.seq;
+    tok = s.tok0 + first;
+    toks = s.n - first;
+    key0 = s.key0;
+    keys = s.keys;
+    tiles = paged_tiles(p, PAGED_FEW, s.keys);
+    before = s.causal ? s.keys - toks : -1;
+    which = p.shared_len > 0 && seg == 0 ? 0 : 1;
+  }
+  DG_HD void range(const PagedShape &p, int done) {   // `done`: cost of the item before the range
+    const int c = p.start_cost[PAGED_FEW], a = done - c, b = done + left - c;
+    t0 = a > 0 ? a : 0;
+    t1 = b < tiles ? b : tiles;
+  }
+  DG_HD void next(const PagedShape &p) {
+    t0 = t1 = 0;
+    if (left <= 0) return;
+    if (++head == p.Hkv) {
+      head = 0;
+      PagedSeg s;
+      do {  // cost remains, so a later segment has an item
+        s = paged_seg(p, ++seg);
+      } while (s.n == 0 || paged_tail_kind(p, s) != PAGED_FEW);
+      take(p, s);
+    }
+    range(p, 0);
+    left -= tiles + p.start_cost[PAGED_FEW];
+  }
+  DG_HD void begin(const PagedShape &p, const PagedStart &st) {
+    t0 = t1 = 0;
+    left = st.u1 - st.u0;
+    if (left <= 0) return;
+    seg = st.seg;
+    head = st.head;
+    take(p, st.s);
+    range(p, st.u0 - st.item_u0);
+    left -= tiles + p.start_cost[PAGED_FEW] - (st.u0 - st.item_u0);
+    if (t0 >= t1) next(p);   // (a range that ends within the first item's starting cost ends here)
+  }
+};
+
 }  // namespace dg

@@ -152,6 +152,18 @@ int main() {
           ++pieces;
         }
         (void)open_tiles;
+        if (kind == 2) {                       // the short walk sees the same pieces
+          PagedFewWalk f;
+          f.begin(p, st);
+          for (w.begin(p, kind, st); w.more(); w.next(p), f.next(p)) {
+            CHECK(f.more() && f.t0 == w.t0 && f.t1 == w.t1 && f.tiles == w.tiles && f.head == w.head);
+            CHECK(f.seg == w.seg && f.seq == w.s.seq && f.tok == w.s.tok0 + w.tok && f.toks == w.toks);
+            CHECK(f.key0 == w.s.key0 && f.keys == w.keys && f.whole() == w.whole());
+            CHECK(f.before == (w.s.causal ? w.s.keys - w.s.n + w.tok : -1));
+            CHECK(f.which == (p.shared_len > 0 && w.seg == 0 ? 0 : 1));
+          }
+          CHECK(!f.more());
+        }
         CHECK((hd.first >= 0) == goes_on);
         CHECK(slots[0] <= 1 && slots[1] <= 1);
       }
