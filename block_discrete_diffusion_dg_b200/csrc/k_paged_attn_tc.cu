@@ -45,6 +45,7 @@ namespace {
 constexpr int P_THR = 384;
 constexpr int P_HALF = 128 * 128;          // 128 rows of 64 bf16 (128-byte rows): 16 KB
 constexpr uint32_t P_COL_S = 0, P_COL_O = 256, P_TMEM = 512;
+constexpr int P_EMU = 1000;                  // of so many pairs of exponentials one is computed by ex2_fma
 constexpr float P_RESCALE = 8.f;           // log2 of the largest P between rescales
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int P_STAGE = 32 * 32 * 4;       // a softmax warp's 32 rows x 32 columns on their way out
@@ -56,6 +57,11 @@ static_assert(P_THR * P_REGS <= 65536, "launch registers");
 
 constexpr int F_KT = PAGED_TC_FEW_KT;      // few-row items: keys per step,
 constexpr int F_SLOTS = 3;                 // slots of a warp's ring, K and V of a step in turn
+
+template <bool B>
+struct Bool {
+  static constexpr bool value = B;
+};
 
 template <int HD>
 struct Tc {
@@ -85,6 +91,23 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// 2^x of two numbers in [-126, 128) by arithmetic: x = n + f with n the nearest integer, 2^f on
+// [-1/2, 1/2] by a polynomial of degree 4 (least squares of the relative error, reweighted to level
+// its peaks: 2.7e-6), n added to the exponent.
+__device__ __forceinline__ float2 ex2_fma(float2 x) {
+  constexpr float MAGIC = 12582912.f;   // 1.5 * 2^23: the sum's last bits are n
+  x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
+  const float2 r = __fadd2_rn(x, make_float2(MAGIC, MAGIC));
+  const float2 n = __fadd2_rn(r, make_float2(-MAGIC, -MAGIC));
+  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
+  float2 q = __ffma2_rn(make_float2(0.009570100344717503f, 0.009570100344717503f), f,
+                        make_float2(0.05591785907745361f, 0.05591785907745361f));
+  q = __ffma2_rn(q, f, make_float2(0.240247443318367f, 0.240247443318367f));
+  q = __ffma2_rn(q, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
+  q = __ffma2_rn(q, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
+  return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(r.x) << 23)),
+                     __int_as_float(__float_as_int(q.y) + (__float_as_int(r.y) << 23)));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -122,6 +145,16 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 // 3-D tiled load of the box at (x = element, y, z).
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int x,
@@ -168,7 +201,8 @@ __global__ void __launch_bounds__(P_THR, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   static_assert((4 + 2 * S + 10) * 8 + PAGED_STARTS * sizeof(PagedStart) + 8 <= 2048, "shared memory");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the shuffle tells the compiler that a warp's threads agree on it)
+  const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (warp == 1) {
     if (lane == 0) {
       for (int x = 0; x < 2; ++x) {
@@ -202,7 +236,7 @@ __global__ void __launch_bounds__(P_THR, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(FULL, *tmem_slot, 0);
   if (threadIdx.x == 0 && blockIdx.x == 0) paged_report(io, err);
   const int rep = io.rep, qn = p.qn;   // qn tokens of rep heads make a query tile
 
@@ -295,7 +329,7 @@ __global__ void __launch_bounds__(P_THR, 1)
     for (int x = 0; x < 2; ++x)
       if (nq[x] > 0) (void)mbar_wait(&q_full[x], (nq[x] - 1) & 1);
   } else if (warp == 1) {
-    // ---- matrix products: the warp waits together, lane 0 issues
+    // ---- matrix products: the warp waits together, one lane issues
     reg_dec<P_REGS_LO>();
     constexpr uint32_t id_s = idesc_bf16(128, KT), id_p = idesc_bf16_bmn(128, HD);
     const uint64_t dq = sdesc_sw128(sQ), dk = sdesc_sw128(sKV), dv = sdesc_sw128_mn(sKV, P_HALF);
@@ -307,12 +341,14 @@ __global__ void __launch_bounds__(P_THR, 1)
       fence_after();
     };
     auto wait_fill = [&](uint32_t f) { wait(&full[f % S], (f / S) & 1); };
+    const bool leader = elect_one();   // the lane that issues
     auto release = [&](uint64_t *bar) {
-      if (ok && lane == 0) commit(bar);
+      if (ok && leader) commit(bar);
     };
     auto issue_s = [&](int x, uint32_t f) {   // S_x = Q_x K^T, K in fill f
-      if (ok && lane == 0) {
-        const uint64_t ab = dq + (uint64_t)((x * TILE) >> 4), bb = dk + (uint64_t)(((f % S) * TILE) >> 4);
+      const uint32_t stage = __shfl_sync(FULL, f % S, 0);
+      const uint64_t ab = dq + (uint64_t)((x * TILE) >> 4), bb = dk + (uint64_t)((stage * TILE) >> 4);
+      if (ok && leader) {
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * P_HALF) >> 4) + 2 * (kk & 3);
@@ -326,8 +362,9 @@ __global__ void __launch_bounds__(P_THR, 1)
       wait(&p_full[x], pn[x] & 1);
       ++pn[x];
       if (first && pieces[x] > 1) wait(&o_empty[x], pieces[x] & 1);   // of the piece before
-      if (ok && lane == 0) {
-        const uint64_t bb = dv + (uint64_t)(((f % S) * TILE) >> 4);
+      const uint32_t stage = __shfl_sync(FULL, f % S, 0);
+      const uint64_t bb = dv + (uint64_t)((stage * TILE) >> 4);
+      if (ok && leader) {
 #pragma unroll
         for (int kk = 0; kk < KT / 16; ++kk)
           mma_f16_ts(tmem + P_COL_O + x * 128, tmem + P_COL_S + x * 128 + kk * 8,
@@ -419,7 +456,7 @@ __global__ void __launch_bounds__(P_THR, 1)
         if (__any_sync(FULL, *abort_flag != 0)) ok = false;
       }
     }
-    if (lane == 0) {
+    if (leader) {
       if (!ok) p_fail(io.status, abort_flag);
       commit(mma_fin);   // every MMA issued above has completed when this phase does
       (void)mbar_wait(mma_fin, 0);
@@ -466,7 +503,8 @@ __global__ void __launch_bounds__(P_THR, 1)
             tmem_ld64(tS + 64, sb);
             tmem_ld_wait64(sa);
             tmem_ld_wait64(sb);
-            if (__any_sync(FULL, lim < KT)) {
+            const bool masked = __any_sync(FULL, lim < KT);
+            if (masked) {
 #pragma unroll
               for (int j = 0; j < 64; ++j) {
                 if (j >= lim) sa[j] = __float_as_uint(-INFINITY);
@@ -506,21 +544,32 @@ __global__ void __launch_bounds__(P_THR, 1)
             const float nb = m_use == -INFINITY ? 0.f : -m_use;
             const float2 sl2v = make_float2(sl2, sl2), nbv = make_float2(nb, nb);
             float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            auto emit = [&](const uint32_t (&v)[64], int hf) {
+            // P of 64 keys.  The special-function unit gives 4 exponentials a cycle and scheduler,
+            // 2048 cycles for the 256 rows of both chains, as long as their matrix products take; one
+            // pair of EMU is computed on the other pipes instead (not where keys are masked: their 2^x
+            // has to be an exact zero).
+            auto emit = [&](const uint32_t (&v)[64], int hf, auto emulate) {
               uint32_t pb[32];
 #pragma unroll
               for (int j = 0; j < 64; j += 2) {
                 const float2 t2 = __ffma2_rn(
                     make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sl2v, nbv);
-                const float2 e = make_float2(ex2(t2.x), ex2(t2.y));
+                float2 e;
+                if (decltype(emulate)::value && (j >> 1) % P_EMU == P_EMU - 1) e = ex2_fma(t2);
+                else e = make_float2(ex2(t2.x), ex2(t2.y));
                 s2[(j >> 1) & 1] = __fadd2_rn(s2[(j >> 1) & 1], e);
                 const __nv_bfloat162 b = __floats2bfloat162_rn(e.x, e.y);
                 pb[j >> 1] = *reinterpret_cast<const uint32_t *>(&b);
               }
               tmem_st32(tS + hf * 32, pb);
             };
-            emit(sa, 0);
-            emit(sb, 1);
+            if (masked) {
+              emit(sa, 0, Bool<false>());
+              emit(sb, 1, Bool<false>());
+            } else {
+              emit(sa, 0, Bool<true>());
+              emit(sb, 1, Bool<true>());
+            }
             l += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
             tmem_st_wait();
           }
