@@ -36,9 +36,10 @@ __device__ __forceinline__ float4 load4(const bf16 *p) {
 // One CTA walks its range of (item, key tile) units: 64 query rows (token-major, the heads of a
 // group within a token) against tiles of 64 keys.  Thread (tx, ty) of 16 x 16 holds rows 4 ty ..
 // 4 ty + 3: scores of keys tx + 16 j, then output columns.  K and V take turns in one tile buffer,
-// so that two CTAs fit an SM and one computes while the other loads.
+// so that two CTAs fit an SM.
 template <typename T, int HD>
-__global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(PagedShape p, PagedIO io) {
+__global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(const __grid_constant__ PagedShape p,
+                                                                  const __grid_constant__ PagedIO io) {
   pdl_wait();
   pdl_trigger();
   constexpr int LD = HD + 4, LP = S_KT + 4;   // padded rows: conflict-free float4 reads
@@ -47,6 +48,7 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(PagedShape p,
   float *Qs = simt_smem_raw, *KVs = Qs + S_ROWS * LD, *Ps = KVs + S_KT * LD;
   __shared__ PagedStart start[1];
   __shared__ PagedScan scan;
+  __shared__ int row_s[2][S_KT];   // rows of a tile's keys in the pool, -1: none (tiles in turn)
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int err = paged_locate<S_THR>(p, blockIdx.x, gridDim.x, 1, start, io.heads, scan);
   __syncthreads();
@@ -58,7 +60,7 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(PagedShape p,
   for (w.begin(p, PAGED_WIDE, st); w.more(); w.next(p)) {
     const PagedSeg s = w.s;
     const int i0 = w.tok, toks = w.toks, rows = toks * rep, item_keys = w.keys;
-    __syncthreads();  // the last piece's readers of Qs and KVs are done
+    __syncthreads();  // the last piece's readers of Qs and the row list are done
     for (int e = tid; e < S_ROWS * (HD / 4); e += S_THR) {
       const int r = e / (HD / 4), c = e % (HD / 4) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -78,22 +80,43 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(PagedShape p,
 #pragma unroll
       for (int d = 0; d < DPT; ++d) o[i][d] = 0.f;
     }
+    // K and V of a tile pass through registers on their way to the one buffer: V is read while the
+    // scores are computed, the next tile's K while P V is; the pages are looked up a tile ahead.
+    constexpr int NE = S_KT * (HD / 4) / S_THR;   // 4-element groups of a tile per thread
+    float4 pre[NE];
+    auto look_up = [&](int t) {
+      if (tid < S_KT) {
+        const int j = t * S_KT + tid;
+        row_s[t & 1][tid] =
+            t < w.t1 && j < item_keys ? (int)paged_row(io, p, s.seq, w.head, s.key0 + j) : -1;
+      }
+    };
+    auto fetch = [&](const void *pages, int t) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const int e = tid + i * S_THR, row = row_s[t & 1][e / (HD / 4)];
+        pre[i] = row >= 0 ? load4((const T *)pages + (size_t)row * HD + e % (HD / 4) * 4)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    auto put = [&]() {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const int e = tid + i * S_THR;
+        *reinterpret_cast<float4 *>(&KVs[e / (HD / 4) * LD + e % (HD / 4) * 4]) = pre[i];
+      }
+    };
+    look_up(w.t0);
+    __syncthreads();
+    fetch(io.k_pages, w.t0);
     for (int t = w.t0; t < w.t1; ++t) {
       const int j0 = t * S_KT;
-      auto load_tile = [&](const void *pages) {
-        for (int e = tid; e < S_KT * (HD / 4); e += S_THR) {
-          const int r = e / (HD / 4), c = e % (HD / 4) * 4;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (j0 + r < item_keys) {
-            const long long row = paged_row(io, p, s.seq, w.head, s.key0 + j0 + r);
-            if (row >= 0) v = load4((const T *)pages + row * HD + c);
-          }
-          *reinterpret_cast<float4 *>(&KVs[r * LD + c]) = v;
-        }
-      };
+      __syncthreads();   // the last P V has read the buffer
+      put();
+      look_up(t + 1);
+      fetch(io.v_pages, t);
       __syncthreads();
-      load_tile(io.k_pages);
-      __syncthreads();
+      if ((tid >> 5) * 8 < rows) {   // warps without rows only load
       float sc[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -143,9 +166,12 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(PagedShape p,
 #pragma unroll
         for (int d = 0; d < DPT; ++d) o[i][d] *= f;
       }
+      }
+      __syncthreads();   // every thread has read K
+      put();
+      if (t + 1 < w.t1) fetch(io.k_pages, t + 1);
       __syncthreads();
-      load_tile(io.v_pages);
-      __syncthreads();
+      if ((tid >> 5) * 8 >= rows) continue;
 #pragma unroll 2
       for (int k = 0; k < S_KT; k += 4) {
         float4 pr[4];
@@ -302,7 +328,7 @@ __device__ __forceinline__ void join_some(const PagedIO &io, const size_t (&row)
 // (Blocks are few on purpose: most have nothing to do, and a thousand of them cost more than the
 // joining.)
 template <typename T, int HD>
-__global__ void __launch_bounds__(256) paged_join_kernel(PagedIO io, int first) {
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedIO io, int first) {
   pdl_wait();
   pdl_trigger();
   __shared__ float acc_s[8][HD];
@@ -384,7 +410,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedIO io, int first) 
 // Joins each row's result over the shared prefix with the one over its own keys; either may have
 // been cut into pieces.  A warp takes two query heads of a packed row.
 template <typename T, int HD>
-__global__ void __launch_bounds__(256) paged_join_prefix_kernel(PagedShape p, PagedIO io) {
+__global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_constant__ PagedShape p,
+                                                                const __grid_constant__ PagedIO io) {
   pdl_wait();
   pdl_trigger();
   constexpr int NR = 2, NS = 4;

@@ -45,7 +45,6 @@ namespace {
 constexpr int P_THR = 384;
 constexpr int P_HALF = 128 * 128;          // 128 rows of 64 bf16 (128-byte rows): 16 KB
 constexpr uint32_t P_COL_S = 0, P_COL_O = 256, P_TMEM = 512;
-constexpr int P_EMU = 1000;                  // of so many pairs of exponentials one is computed by ex2_fma
 constexpr float P_RESCALE = 8.f;           // log2 of the largest P between rescales
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int P_STAGE = 32 * 32 * 4;       // a softmax warp's 32 rows x 32 columns on their way out
@@ -57,11 +56,6 @@ static_assert(P_THR * P_REGS <= 65536, "launch registers");
 
 constexpr int F_KT = PAGED_TC_FEW_KT;      // few-row items: keys per step,
 constexpr int F_SLOTS = 3;                 // slots of a warp's ring, K and V of a step in turn
-
-template <bool B>
-struct Bool {
-  static constexpr bool value = B;
-};
 
 template <int HD>
 struct Tc {
@@ -91,23 +85,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-// 2^x of two numbers in [-126, 128) by arithmetic: x = n + f with n the nearest integer, 2^f on
-// [-1/2, 1/2] by a polynomial of degree 4 (least squares of the relative error, reweighted to level
-// its peaks: 2.7e-6), n added to the exponent.
-__device__ __forceinline__ float2 ex2_fma(float2 x) {
-  constexpr float MAGIC = 12582912.f;   // 1.5 * 2^23: the sum's last bits are n
-  x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
-  const float2 r = __fadd2_rn(x, make_float2(MAGIC, MAGIC));
-  const float2 n = __fadd2_rn(r, make_float2(-MAGIC, -MAGIC));
-  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
-  float2 q = __ffma2_rn(make_float2(0.009570100344717503f, 0.009570100344717503f), f,
-                        make_float2(0.05591785907745361f, 0.05591785907745361f));
-  q = __ffma2_rn(q, f, make_float2(0.240247443318367f, 0.240247443318367f));
-  q = __ffma2_rn(q, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
-  q = __ffma2_rn(q, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
-  return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(r.x) << 23)),
-                     __int_as_float(__float_as_int(q.y) + (__float_as_int(r.y) << 23)));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -405,12 +382,12 @@ __global__ void __launch_bounds__(P_THR, 1)
         for (int t = w.t0; t < w.t1 && ok; ++t, f += 2) {
           const bool more = t + 1 < w.t1;
           wait_v(f + 1, w.keys - t * KT);
+          if (more) wait_fill(f + 2);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             take_pv(x, f + 1, t == w.t0);
             if (x == 1) release(&empty[(f + 1) % S]);
             if (more) {
-              if (x == 0) wait_fill(f + 2);
               issue_s(x, f + 2);
               if (t + 2 == w.t1) release(&q_empty[x]);
               if (x == 1) release(&empty[(f + 2) % S]);
@@ -503,8 +480,7 @@ __global__ void __launch_bounds__(P_THR, 1)
             tmem_ld64(tS + 64, sb);
             tmem_ld_wait64(sa);
             tmem_ld_wait64(sb);
-            const bool masked = __any_sync(FULL, lim < KT);
-            if (masked) {
+            if (__any_sync(FULL, lim < KT)) {
 #pragma unroll
               for (int j = 0; j < 64; ++j) {
                 if (j >= lim) sa[j] = __float_as_uint(-INFINITY);
@@ -544,32 +520,21 @@ __global__ void __launch_bounds__(P_THR, 1)
             const float nb = m_use == -INFINITY ? 0.f : -m_use;
             const float2 sl2v = make_float2(sl2, sl2), nbv = make_float2(nb, nb);
             float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            // P of 64 keys.  The special-function unit gives 4 exponentials a cycle and scheduler,
-            // 2048 cycles for the 256 rows of both chains, as long as their matrix products take; one
-            // pair of EMU is computed on the other pipes instead (not where keys are masked: their 2^x
-            // has to be an exact zero).
-            auto emit = [&](const uint32_t (&v)[64], int hf, auto emulate) {
+            auto emit = [&](const uint32_t (&v)[64], int hf) {   // P of 64 keys
               uint32_t pb[32];
 #pragma unroll
               for (int j = 0; j < 64; j += 2) {
                 const float2 t2 = __ffma2_rn(
                     make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sl2v, nbv);
-                float2 e;
-                if (decltype(emulate)::value && (j >> 1) % P_EMU == P_EMU - 1) e = ex2_fma(t2);
-                else e = make_float2(ex2(t2.x), ex2(t2.y));
+                const float2 e = make_float2(ex2(t2.x), ex2(t2.y));
                 s2[(j >> 1) & 1] = __fadd2_rn(s2[(j >> 1) & 1], e);
                 const __nv_bfloat162 b = __floats2bfloat162_rn(e.x, e.y);
                 pb[j >> 1] = *reinterpret_cast<const uint32_t *>(&b);
               }
               tmem_st32(tS + hf * 32, pb);
             };
-            if (masked) {
-              emit(sa, 0, Bool<false>());
-              emit(sb, 1, Bool<false>());
-            } else {
-              emit(sa, 0, Bool<true>());
-              emit(sb, 1, Bool<true>());
-            }
+            emit(sa, 0);
+            emit(sb, 1);
             l += (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y);
             tmem_st_wait();
           }
