@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(const __grid_
   __shared__ PagedScan scan;
   __shared__ int row_s[2][S_KT];   // rows of a tile's keys in the pool, -1: none (tiles in turn)
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int err = paged_locate<S_THR>(p, blockIdx.x, gridDim.x, 1, start, io.heads, scan);
+  const int err = paged_locate<S_THR, 1>(p, blockIdx.x, gridDim.x, 1, start, io.heads, scan);
   __syncthreads();
   const PagedStart st = start[0];
   if (tid == 0 && blockIdx.x == 0) paged_report(io, err);
@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(const __grid_
       const int r = e / (HD / 4), c = e % (HD / 4) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows)
-        v = load4((const T *)io.q +
-                  ((size_t)(s.tok0 + i0 + r / rep) * io.Hq + w.head * rep + r % rep) * HD + c);
+        v = load4((const T *)io.q + ((size_t)(s.tok0 + i0 + paged_token(io, r)) * io.Hq + w.head * rep +
+                                     r - paged_token(io, r) * rep) * HD + c);
       *reinterpret_cast<float4 *>(&Qs[r * LD + c]) = v;
     }
     float o[4][DPT], m[4], l[4];
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(const __grid_
       const int r = ty * 4 + i;
       m[i] = -INFINITY;
       l[i] = 0.f;
-      lim[i] = s.causal ? s.keys - s.n + i0 + min(r / rep, toks - 1) + 1 : s.keys;
+      lim[i] = s.causal ? s.keys - s.n + i0 + min(paged_token(io, r), toks - 1) + 1 : s.keys;
 #pragma unroll
       for (int d = 0; d < DPT; ++d) o[i][d] = 0.f;
     }
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(const __grid_
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
       if (r >= rows) continue;
-      const int tok = s.tok0 + i0 + r / rep, h = w.head * rep + r % rep;
+      const int tl = paged_token(io, r), tok = s.tok0 + i0 + tl, h = w.head * rep + r - tl * rep;
       if (dest.kind == PAGED_OUT) {
         const float il = l[i] > 0.f ? 1.f / l[i] : 0.f;
         T *dst = (T *)io.out + ((size_t)tok * io.Hq + h) * HD;
@@ -322,25 +322,31 @@ __device__ __forceinline__ void join_some(const PagedIO &io, const size_t (&row)
 }
 
 // Joins the items that range boundaries cut.  The workers that go on with an item share its rows: of
-// wide and narrow items each has two blocks, of few-row ones eight have one.  Where an item of few rows
+// wide items each has two blocks, of narrow ones one, of few-row ones eight have one.  Where an item of few rows
 // was cut for many workers (one long context), the warps of a block share the pieces of a row and join
 // once more through shared memory; else a warp takes whole rows.
 // (Blocks are few on purpose: most have nothing to do, and a thousand of them cost more than the
 // joining.)
+struct JoinBlocks {
+  int wide, few;   // blocks for wide and few-row items; the rest are for narrow ones
+};
 template <typename T, int HD>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedIO io, int first) {
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedIO io, JoinBlocks blocks) {
   pdl_wait();
   pdl_trigger();
   __shared__ float acc_s[8][HD];
   __shared__ float2 ml_s[8];
   constexpr int MANY = 16;   // pieces worth sharing
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wide = 3 * io.ctas - first;   // workers with two blocks, from `first` on
-  const bool few = (int)blockIdx.x >= 2 * wide;
-  const int c0 = few ? 3 * io.ctas + (blockIdx.x - 2 * wide) * 8 : first + blockIdx.x / 2;
+  // blocks: two for each wide worker, one for eight few-row ones, one for each narrow one
+  const int b_few = blockIdx.x - blocks.wide, b_narrow = b_few - blocks.few;
+  const bool few = b_few >= 0 && b_narrow < 0;
+  const int shares = b_few < 0 ? 2 : 1;   // blocks of a wide or narrow worker
+  const int c0 = b_few < 0 ? blockIdx.x / 2 : few ? 3 * io.ctas + b_few * 8 : io.ctas + b_narrow;
   const int c = few ? c0 + warp : c0, base = paged_first_worker(io, paged_worker_kind(io, c));
   auto out = [&](const PagedHead &h, int r) {
-    return (T *)io.out + ((size_t)(h.tok0 + r / io.rep) * io.Hq + h.head * io.rep + r % io.rep) * HD;
+    const int tl = paged_token(io, r);
+    return (T *)io.out + ((size_t)(h.tok0 + tl) * io.Hq + h.head * io.rep + r - tl * io.rep) * HD;
   };
   {
     const PagedHead h = io.heads[c];
@@ -349,8 +355,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     // this warp's rows r0, r0 + step, ... of the item's shares
     int r0 = c - begin - 1, step = n - 1;
     if (!few) {
-      r0 = (r0 * 2 + (blockIdx.x & 1)) * 8 + warp;
-      step *= 16;
+      r0 = (r0 * shares + (shares == 2 ? blockIdx.x & 1 : 0)) * 8 + warp;
+      step *= 8 * shares;
     }
     if (n == 2) {
       constexpr int NR = 4;
@@ -440,7 +446,7 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_con
   T *dst[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
-    const int h = min(h0 + i, io.Hq - 1);
+    const int h = min(h0 + i, io.Hq - 1), hr = h % io.rep;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       row[i][2 * k] = row[i][2 * k + 1] = paged_region_row(p, io, k, tok, h);
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_con
         const int c = __float_as_int(ml[i][k].x);
         const PagedHead hd = io.heads[c + 1];
         many = many || hd.last > hd.first + 1;
-        const int r = (tok - hd.tok0) * io.rep + h % io.rep;
+        const int r = (tok - hd.tok0) * io.rep + hr;
         row[i][2 * k] = paged_slot_row(io, c, true, r);
         row[i][2 * k + 1] = paged_slot_row(io, c + 1, false, r);
       }
@@ -463,6 +469,7 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_con
   }
 #pragma unroll 1
   for (int h = h0; h < min(h0 + NR, io.Hq); ++h) {
+    const int hr = h % io.rep;
     Fold<HD> f;
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
@@ -472,7 +479,7 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_con
         const int c = __float_as_int(e.x);
         const PagedHead hd = io.heads[c + 1];
         f.add_range(io, c, c, hd.last + paged_first_worker(io, paged_worker_kind(io, c)),
-                    (tok - hd.tok0) * io.rep + h % io.rep);
+                    (tok - hd.tok0) * io.rep + hr);
       } else {
         f.add(io.part_o, 1, e, r);
       }
@@ -500,10 +507,10 @@ int run_join(const PagedShape &p, const PagedIO &io, cudaStream_t s) {
   }
   // no item of a kind can exist with fewer rows than it takes
   const bool tc = io.workers > io.ctas;
-  const int first = !tc || p.n_tokens > p.qn ? 0 : p.n_tokens > p.qf ? io.ctas : 3 * io.ctas;
-  const int blocks = tc ? 2 * (3 * io.ctas - first) + io.ctas : 2 * io.ctas;
+  const JoinBlocks b{!tc || p.n_tokens > p.qn ? 2 * io.ctas : 0, tc ? io.ctas : 0};
+  const int narrow = tc && p.n_tokens > p.qf ? 2 * io.ctas : 0;
   note_launch(s, "paged_join");
-  launch_pdl(paged_join_kernel<T, HD>, blocks, 256, 0, s, io, first);
+  launch_pdl(paged_join_kernel<T, HD>, b.wide + b.few + narrow, 256, 0, s, io, b);
   return check_launch("paged_join");
 }
 
@@ -589,6 +596,7 @@ int launch_paged_attn(const PagedCall &c, void *ws, cudaStream_t s) {
   while ((1 << io.page_shift) < c.page_size) ++io.page_shift;
   io.Hq = c.Hq;
   io.rep = c.Hq / c.Hkv;
+  io.rep_mul = (65536 + io.rep - 1) / io.rep;
   io.heads = (PagedHead *)((char *)ws + l.heads);
   io.part_ml = (float2 *)((char *)ws + l.part_ml);
   io.part_o = (float *)((char *)ws + l.part_o);

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(P_THR, 1)
     tma_prefetch_desc(&tmV);
   }
   // (the scan's scratch lies where rows will leave the kernel much later)
-  const int err = paged_locate<P_THR / 3>(p, blockIdx.x, gridDim.x, PAGED_STARTS, start, io.heads,
+  const int err = paged_locate<P_THR / 3, 3>(p, blockIdx.x, gridDim.x, PAGED_STARTS, start, io.heads,
                                           *reinterpret_cast<PagedScan *>(sOut));
   fence_before();
   __syncthreads();
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(P_THR, 1)
       for (w.begin(p, kind, start[kind == PAGED_WIDE ? 0 : 1 + x]); w.more(); w.next(p)) {
         const int tile0 = kind == PAGED_WIDE ? x * qn : 0;        // first token of the chain's tile
         const int rows = min(qn, w.toks - tile0) * rep;           // at least one token
-        const int tl = tile0 + min(r, rows - 1) / rep;            // this row's token in the item
+        const int tl = tile0 + paged_token(io, min(r, rows - 1)); // this row's token in the item
         const bool warp_on = q4 * 32 < rows;                      // any row of this warp
         const int seen = w.s.causal ? w.s.keys - w.s.n + w.tok + tl + 1 : w.keys;
         float m_use = -INFINITY, l = 0.f;
@@ -561,8 +561,8 @@ __global__ void __launch_bounds__(P_THR, 1)
           // for 256 rows of 128 fp32 columns).
           const int tok_w = w.s.tok0 + w.tok + tile0, h0 = w.head * rep;
           auto dst_row = [&](int i) {   // of row i of this warp
-            const int rr = q4 * 32 + i;
-            return paged_dest_row(io, dest, tile0 * rep + rr, tok_w + rr / rep, h0 + rr % rep);
+            const int rr = q4 * 32 + i, tl = paged_token(io, rr);
+            return paged_dest_row(io, dest, tile0 * rep + rr, tok_w + tl, h0 + rr - tl * rep);
           };
           const size_t base = paged_dest_base(p, io, dest);
           int row8[8];
@@ -595,7 +595,8 @@ __global__ void __launch_bounds__(P_THR, 1)
           }
           if (!out && lane < on) {
             io.part_ml[base + dst_row(lane)] = make_float2(m_use, l);
-            if (dest.redirect) paged_redirect(p, io, dest, worker, tok_w + r / rep, h0 + r % rep);
+            if (dest.redirect)
+              paged_redirect(p, io, dest, worker, w.s.tok0 + w.tok + tl, h0 + r - (tl - tile0) * rep);
           }
         }
         fence_before();
@@ -644,7 +645,7 @@ __global__ void __launch_bounds__(P_THR, 1)
             const bf16 *q[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int rr = min(gr + 8 * i, rows - 1), tl = rr / rep;
+              const int rr = min(gr + 8 * i, rows - 1), tl = paged_token(io, rr);
               q[i] = (const bf16 *)io.q + ((size_t)(pc.tok + tl) * io.Hq + h0 + rr - tl * rep) * HD + tq * 2;
               seen[i] = pc.before < 0 ? pc.keys : pc.before + tl + 1;
               m[i] = -INFINITY;
@@ -752,7 +753,7 @@ __global__ void __launch_bounds__(P_THR, 1)
               ls[i] += __shfl_xor_sync(FULL, ls[i], 2);
               const int rr = gr + 8 * i;
               if (rr >= rows) continue;
-              const int tok = pc.tok + rr / rep, h = h0 + rr % rep;
+              const int tl = paged_token(io, rr), tok = pc.tok + tl, h = h0 + rr - tl * rep;
               const size_t row = base + paged_dest_row(io, dest, rr, tok, h);
               if (dest.kind == PAGED_OUT) {
                 const float il = ls[i] > 0.f ? 1.f / ls[i] : 0.f;

@@ -14,6 +14,7 @@ struct PagedIO {
   const int32_t *page_table;     // [n_seqs][max_pages]
   int n_pages, max_pages, page_shift;
   int Hq, rep;
+  int rep_mul;                   // ceil(2^16 / rep): row / rep by paged_token
   int ctas;
   int workers;                   // of all kinds (see paged_worker)
   int rows[3];                   // rows of a partial result's slot, by kind of item
@@ -35,6 +36,11 @@ constexpr int PAGED_TC_LEAST_FEW = 2;
 inline bool paged_tc_supported(int act, int hd) { return act == DG_BF16 && (hd == 64 || hd == 128); }
 struct PagedCall;
 int launch_paged_tc(const PagedCall &c, const PagedShape &p, const PagedIO &io, cudaStream_t s);
+
+// Row r of an item is head r % rep of its token r / rep.  The quotient by a multiplication (exact for
+// r < 256, rep <= 64: r (rep - 1) < 2^16): rows are turned into tokens and heads in many places, and a
+// division is 20 instructions.
+__device__ __forceinline__ int paged_token(const PagedIO &io, int r) { return (r * io.rep_mul) >> 16; }
 
 // Row (of hd elements) of key `pos` of a sequence in the page pool, -1 (and the status word set)
 // for a page id outside it.

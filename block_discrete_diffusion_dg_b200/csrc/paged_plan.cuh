@@ -226,10 +226,10 @@ struct PagedScan {
   int error;
 };
 
-// Finds the ranges of this CTA's workers for the kinds that have GROUP threads each (thread t works for
-// kind t / GROUP); warp j leaves the j-th worker's in start[j] and its head in heads[].  The block
+// Finds the ranges of this CTA's workers of the first KINDS kinds, with GROUP threads for each (thread t
+// works for kind t / GROUP; further threads take no part); warp j leaves the j-th worker's in start[j] and its head in heads[].  The block
 // synchronises inside, and has to before start is read.  Returns the largest error code of any sequence.
-template <int GROUP>
+template <int GROUP, int KINDS>
 __device__ __forceinline__ int paged_locate(const PagedShape &p, int cta, int ctas, int starts,
                                             PagedStart *start, PagedHead *heads, PagedScan &scan) {
   constexpr unsigned full = 0xffffffffu;
@@ -237,7 +237,7 @@ __device__ __forceinline__ int paged_locate(const PagedShape &p, int cta, int ct
   const int segs = paged_segs(p), chunk = (segs + GROUP - 1) / GROUP;
   if (tid == 0) scan.error = 0;
   __syncthreads();
-  {
+  if (tid < KINDS * GROUP) {
     const int kind = tid / GROUP, t = tid % GROUP;
     int mine = 0;   // cost of this thread's sequences
     for (int i = t * chunk; i < min((t + 1) * chunk, segs); ++i) {
