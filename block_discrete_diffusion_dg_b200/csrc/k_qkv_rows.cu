@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(Q_THR) qkv_rows_kernel(const __grid_constant__
         const unsigned mask = ((1u << LPH) - 1u) << ((tid & 31) / LPH * LPH);
 #pragma unroll
         for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-        const float rs = 1.f / sqrtf(ss * (1.f / HD) + a.eps);
+        const float rs = rsqrtf(ss * (1.f / HD) + a.eps);
         Chunk<float> ga, gb;
         float g[8];
         ga.load(gain + ca * 8);
