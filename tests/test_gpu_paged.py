@@ -276,6 +276,69 @@ def test_prefix_attn(act, hq, hkv, hd, batch, causal):
     check_attention(out, q, c, new, have, causal, act)
 
 
+def random_batch(rng, seqs, big):
+    """New tokens and cached keys of a random batch: single tokens, tails, chunks and prompts."""
+    kinds = [lambda: 1, lambda: rng.randint(1, 20), lambda: rng.randint(1, big), lambda: 0]
+    new = [rng.choice(kinds)() for _ in range(seqs)]
+    have = [rng.choice((0, 1, rng.randint(0, 40), rng.randint(0, 8 * big))) for _ in range(seqs)]
+    if sum(new) == 0:
+        new[0] = 1
+    return new, have
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    """All kinds of work in one call: sequences of many lengths, any head group, page size and mask,
+    with and without a shared prefix."""
+    rng = random.Random(seed)
+    act, hd = rng.choice((("bf16", 128), ("bf16", 64), ("f32", 64)))
+    hkv = rng.choice((1, 2, 3))
+    hq = hkv * rng.choice((1, 2, 3, 4, 7, 8, 17))
+    page = rng.choice((16, 32, 128, 256))
+    seqs = rng.choice((1, 5, 40, 140, 400))
+    new, have = random_batch(rng, seqs, 300 if seqs < 20 else 30)
+    shared = page * rng.randint(1, 4) if seed % 3 == 2 else 0
+    have = [shared + h for h in have]
+    g = gen(seed)
+    c = Cache(g, act, hkv, hd, page, [n + h for n, h in zip(new, have)], shared=shared)
+    q = (1.5 * randn(g, sum(new) + 1, hq, hd)).to(DT[act])
+    for causal in (0, 1):
+        out, st = run_attention(make_cfg(act, hq, hkv, hd), c, new, have, q, causal, shared=shared)
+        assert st == B.DG_OK
+        check_attention(out, q, c, new, have, causal, act)
+
+
+@pytest.mark.parametrize("n_new", [1, 40, 200])
+def test_pages_past_32_bit_offsets(n_new):
+    """A pool of more than 2^31 elements: the sequence's pages lie at its far end."""
+    g, hkv, hd, page, have = gen(77), 8, 128, 64, 200
+    n_pages = (1 << 31) // (hkv * page * hd) + 64
+    pools = [torch.empty(n_pages, hkv, page, hd, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    keys = have + n_new
+    used = -(-keys // page)
+    table = torch.arange(n_pages - used, n_pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    for t in pools:
+        t[n_pages - used:] = math.nan
+    kv = B.PagedKV(*pools, table)
+    cfg = make_cfg("bf16", 16, hkv, hd)
+    k, v = (randn(g, keys, hkv, hd).to(torch.bfloat16) for _ in range(2))
+    qkv = torch.cat((torch.zeros(keys, 16 * hd, device="cuda", dtype=torch.bfloat16),
+                     k.view(keys, -1), v.view(keys, -1)), 1)
+    st = i32([0])
+    B.dg_paged_append(cfg, 1, keys, i32([0, keys]), i32([0]), qkv, None, None, B.make_rope(0), kv,
+                      None, st)
+    pos = torch.arange(keys, device="cuda")
+    ids = table[0][pos // page].long()
+    assert torch.equal(pools[0][ids, :, pos % page], k) and torch.equal(pools[1][ids, :, pos % page], v)
+    q = randn(g, n_new, 16, hd).to(torch.bfloat16)
+    out = torch.empty_like(q)
+    ws = B.alloc_paged_workspace(cfg, 1, n_new)
+    B.dg_paged_attn(cfg, 1, n_new, i32([0, n_new]), i32([have]), q, kv, 1, out, ws, st)
+    assert B.dg_read_status(st) == B.DG_OK
+    want, A, e = P.attention(q, k, v, 1, have)
+    assert P.worst(out, want, P.attention_bound(want, A, e, keys, torch.bfloat16, 2.0 ** -8)) <= 1.0
+
+
 @pytest.mark.parametrize("act,hq,hkv,hd", [("bf16", 16, 8, 128), ("f32", 4, 2, 64)])
 def test_extreme_scores(act, hq, hkv, hd):
     """Scores far apart and growing along the keys: the running maximum moves on and late keys
