@@ -117,55 +117,55 @@ __global__ void __launch_bounds__(S_THR, 2) paged_attn_simt_kernel(const __grid_
       fetch(io.v_pages, t);
       __syncthreads();
       if ((tid >> 5) * 8 < rows) {   // warps without rows only load
-      float sc[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
-#pragma unroll 4
-      for (int d = 0; d < HD; d += 4) {
-        float4 a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = *reinterpret_cast<const float4 *>(&Qs[(ty * 4 + i) * LD + d]);
-          b[i] = *reinterpret_cast<const float4 *>(&KVs[(tx + 16 * i) * LD + d]);
-        }
+        float sc[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sc[i][j] = fmaf(a[i].x, b[j].x, sc[i][j]);
-            sc[i][j] = fmaf(a[i].y, b[j].y, sc[i][j]);
-            sc[i][j] = fmaf(a[i].z, b[j].z, sc[i][j]);
-            sc[i][j] = fmaf(a[i].w, b[j].w, sc[i][j]);
+          for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < HD; d += 4) {
+          float4 a[4], b[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = *reinterpret_cast<const float4 *>(&Qs[(ty * 4 + i) * LD + d]);
+            b[i] = *reinterpret_cast<const float4 *>(&KVs[(tx + 16 * i) * LD + d]);
           }
-      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float mt = -INFINITY;
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sc[i][j] = j0 + tx + 16 * j < lim[i] ? sc[i][j] * sl2 : -INFINITY;
-          mt = fmaxf(mt, sc[i][j]);
+            for (int j = 0; j < 4; ++j) {
+              sc[i][j] = fmaf(a[i].x, b[j].x, sc[i][j]);
+              sc[i][j] = fmaf(a[i].y, b[j].y, sc[i][j]);
+              sc[i][j] = fmaf(a[i].z, b[j].z, sc[i][j]);
+              sc[i][j] = fmaf(a[i].w, b[j].w, sc[i][j]);
+            }
         }
 #pragma unroll
-        for (int b = 8; b > 0; b >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, b));
-        const float mn = fmaxf(m[i], mt), base = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m[i] - base);
-        m[i] = mn;
-        float ps = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          float mt = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float e = exp2f(sc[i][j] - base);
-          ps += e;
-          Ps[(ty * 4 + i) * LP + tx + 16 * j] = e;
+          for (int j = 0; j < 4; ++j) {
+            sc[i][j] = j0 + tx + 16 * j < lim[i] ? sc[i][j] * sl2 : -INFINITY;
+            mt = fmaxf(mt, sc[i][j]);
+          }
+#pragma unroll
+          for (int b = 8; b > 0; b >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, b));
+          const float mn = fmaxf(m[i], mt), base = mn == -INFINITY ? 0.f : mn;
+          const float f = exp2f(m[i] - base);
+          m[i] = mn;
+          float ps = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float e = exp2f(sc[i][j] - base);
+            ps += e;
+            Ps[(ty * 4 + i) * LP + tx + 16 * j] = e;
+          }
+#pragma unroll
+          for (int b = 8; b > 0; b >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, b);
+          l[i] = l[i] * f + ps;
+#pragma unroll
+          for (int d = 0; d < DPT; ++d) o[i][d] *= f;
         }
-#pragma unroll
-        for (int b = 8; b > 0; b >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, b);
-        l[i] = l[i] * f + ps;
-#pragma unroll
-        for (int d = 0; d < DPT; ++d) o[i][d] *= f;
-      }
       }
       __syncthreads();   // every thread has read K
       put();
