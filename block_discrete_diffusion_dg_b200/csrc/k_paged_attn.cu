@@ -279,8 +279,8 @@ struct Fold {
   }
 };
 
-// NR rows at once, each of NS partial results (NR x NS loads in flight).  row[i][k]: rows of part_o, on:
-// whether they count; dst[i]: output row, or null.
+// NR rows at once, each of NS partial results (NR x NS loads in flight).  row[i][k]: rows of
+// part_o, on: whether they count; dst[i]: output row, or null.
 template <typename T, int HD, int NR, int NS>
 __device__ __forceinline__ void join_some(const PagedIO &io, const size_t (&row)[NR][NS],
                                           const bool (&on)[NR][NS], T *const (&dst)[NR]) {
@@ -321,12 +321,11 @@ __device__ __forceinline__ void join_some(const PagedIO &io, const size_t (&row)
   }
 }
 
-// Joins the items that range boundaries cut.  The workers that go on with an item share its rows: of
-// wide items each has two blocks, of narrow ones one, of few-row ones eight have one.  Where an item of few rows
-// was cut for many workers (one long context), the warps of a block share the pieces of a row and join
-// once more through shared memory; else a warp takes whole rows.
-// (Blocks are few on purpose: most have nothing to do, and a thousand of them cost more than the
-// joining.)
+// Joins the items that range boundaries cut.  The workers that go on with an item share its rows:
+// of wide items each has two blocks, of narrow ones one, of few-row ones eight have one.  Where an
+// item of few rows was cut for many workers (one long context), the warps of a block share the
+// pieces of a row and join once more through shared memory; else a warp takes whole rows. (Blocks
+// are few on purpose: most have nothing to do, and a thousand of them cost more than the joining.)
 struct JoinBlocks {
   int wide, few;   // blocks for wide and few-row items; the rest are for narrow ones
 };

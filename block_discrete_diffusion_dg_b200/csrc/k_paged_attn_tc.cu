@@ -2,36 +2,36 @@
 // 128).  "DiffusionGemma Technical Report", Figure 4; the mathematics and the joining of partial
 // results stand in k_paged_attn.cu, the split of the work in paged_plan.cuh.
 //
-// Query rows are token-major: row r of a tile is token r / rep, head r % rep of one kv head's group,
-// so every K/V tile is read once per group and any group size fits a tile of 128 rows.  One CTA per
-// SM runs two chains of
+// Query rows are token-major: row r of a tile is token r / rep, head r % rep of one kv head's
+// group, so every K/V tile is read once per group and any group size fits a tile of 128 rows.  One
+// CTA per SM runs two chains of
 //   S_x = Q_x K^T    (128 x 128 keys x head_dim, bf16 from shared memory)
 //   P_x = softmax's numerators, O_x += P_x V    (P from tensor memory, V from shared memory)
 // so that the softmax of one overlaps the matrix products of the other:
 //   wide items     both chains take one query tile each (up to 256 rows) against the same key tiles;
 //   narrow items   (short prompts, tails: up to 128 rows) each chain walks a range of its own, so that
 //                  the start and end of one's items hide behind the other's work.
-// Few-row items (single tokens: up to 16 rows) would leave 7/8 of such a tile empty and pass each key
-// tile through a chain of four waits; there each of the eight softmax warps walks a range of its own
-// with mma.sync, 32 keys a step, from a ring of its own in the memory that the chains have left, so
-// that almost all of it is in flight: these items are bound by the bytes of their keys.  Their copies
-// are cp.async, not TMA: a box of one 16-key page takes the TMA unit about 60 cycles for 2 KB, and eight
-// warps that each wait for several such boxes waited 3 us before their first product.
-// Tensor memory (512 columns): S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512); P_x is
-// written over S_x.  MMAs of one thread execute in issue order, so S_x of the next key tile is
-// issued right behind P_x V.
+// Few-row items (single tokens: up to 16 rows) would leave 7/8 of such a tile empty and pass each
+// key tile through a chain of four waits; there each of the eight softmax warps walks a range of
+// its own with mma.sync, 32 keys a step, from a ring of its own in the memory that the chains have
+// left, so that almost all of it is in flight: these items are bound by the bytes of their keys.
+// Their copies are cp.async, not TMA: a box of one 16-key page takes the TMA unit about 60 cycles
+// for 2 KB, and eight warps that each wait for several such boxes waited 3 us before their first
+// product. Tensor memory (512 columns): S_A [0,128), S_B [128,256), O_A [256,384), O_B [384,512);
+// P_x is written over S_x.  MMAs of one thread execute in issue order, so S_x of the next key tile
+// is issued right behind P_x V.
 //
 // P is rounded to bf16, as V is given: a relative error up to 2^-8 in each p, independent from key
 // to key, which adds to an output about as much as its own rounding does (measured: 0.0024 of the
 // outputs' size against 0.0017 for the rounding alone).  Two bf16 parts would cost a second P V
 // product, 1.5 times the tensor work.
 //
-// Warps: 0 copies (one lane per page: each looks its page up and issues that page's TMA boxes into a
-// ring of key / value tiles), 1 owns the tensor memory and issues the MMAs, 4-7 are the softmax of
-// chain A and 8-11 of chain B, a query row per thread.  What a page holds behind a sequence's last
-// key is masked in S and zeroed in V before the product reads it (0 * NaN).
-// Every wait is bounded; on expiry the kernel records DG_ERR_TIMEOUT, lets issued copies and MMAs
-// finish, frees tensor memory and returns.
+// Warps: 0 copies (one lane per page: each looks its page up and issues that page's TMA boxes into
+// a ring of key / value tiles), 1 owns the tensor memory and issues the MMAs, 4-7 are the softmax
+// of chain A and 8-11 of chain B, a query row per thread.  What a page holds behind a sequence's
+// last key is masked in S and zeroed in V before the product reads it (0 * NaN). Every wait is
+// bounded; on expiry the kernel records DG_ERR_TIMEOUT, lets issued copies and MMAs finish, frees
+// tensor memory and returns.
 #include "dg_common.cuh"
 #include "dg_kernels.h"
 #include "paged_attn.cuh"
@@ -615,10 +615,11 @@ __global__ void __launch_bounds__(P_THR, 1)
       uint8_t *ring = sQ + fw * F_SLOTS * SLOT;
       const int shift = io.page_shift;
       ok = __all_sync(FULL, mbar_wait(chains_done, 0));
-      // Copies run F_SLOTS slots ahead of the arithmetic, across items: slot n of the walk is K (n even)
-      // or V of a step, one group of cp.async each.  Rows behind the last key are filled with zeros.
-      // Each lane holds the first row (for kv head 0) of a page, 32 pages of a sequence at a time.
-      // The loading side walks the items and leaves each piece's description for the computing side.
+      // Copies run F_SLOTS slots ahead of the arithmetic, across items: slot n of the walk is K (n
+      // even) or V of a step, one group of cp.async each.  Rows behind the last key are filled
+      // with zeros. Each lane holds the first row (for kv head 0) of a page, 32 pages of a
+      // sequence at a time. The loading side walks the items and leaves each piece's description
+      // for the computing side.
       PagedFewWalk lw;
       lw.begin(p, few_start);
       int lt = lw.t0, ids = 0, ids_seg = -1, ids_page = 0;

@@ -37,9 +37,9 @@ inline bool paged_tc_supported(int act, int hd) { return act == DG_BF16 && (hd =
 struct PagedCall;
 int launch_paged_tc(const PagedCall &c, const PagedShape &p, const PagedIO &io, cudaStream_t s);
 
-// Row r of an item is head r % rep of its token r / rep.  The quotient by a multiplication (exact for
-// r < 256, rep <= 64: r (rep - 1) < 2^16): rows are turned into tokens and heads in many places, and a
-// division is 20 instructions.
+// Row r of an item is head r % rep of its token r / rep.  The quotient by a multiplication (exact
+// for r < 256, rep <= 64: r (rep - 1) < 2^16): rows are turned into tokens and heads in many
+// places, and a division is 20 instructions.
 __device__ __forceinline__ int paged_token(const PagedIO &io, int r) { return (r * io.rep_mul) >> 16; }
 
 // Row (of hd elements) of key `pos` of a sequence in the page pool, -1 (and the status word set)
@@ -58,9 +58,10 @@ __device__ __forceinline__ void paged_report(const PagedIO &io, int error) {
   if (error) set_status(io.status, error == 2 ? DG_ERR_CAPACITY : DG_ERR_INVALID_ARG);
 }
 
-// ---- destinations -------------------------------------------------------------------------------
-// Workers are numbered through: wide ones [0, ctas), narrow ones (two per CTA) [ctas, 3 ctas), few-row
-// ones (eight per CTA) [3 ctas, 11 ctas).
+// ---- destinations
+// ------------------------------------------------------------------------------- Workers are
+// numbered through: wide ones [0, ctas), narrow ones (two per CTA) [ctas, 3 ctas), few-row ones
+// (eight per CTA) [3 ctas, 11 ctas).
 __host__ __device__ inline int paged_first_worker(const PagedIO &io, int kind) {
   return kind == PAGED_WIDE ? 0 : kind == PAGED_NARROW ? io.ctas : 3 * io.ctas;
 }
@@ -89,9 +90,9 @@ __device__ __forceinline__ size_t paged_region_row(const PagedShape &p, const Pa
   return io.region + ((size_t)which * p.n_tokens + tok) * io.Hq + h;
 }
 
-// Where a piece goes: a whole item to the output (or its half of the region), a part of one to a slot
-// of this worker (slot 1 if the item begins here, slot 0 if it goes on from an earlier worker; a range
-// holds at most one of each).
+// Where a piece goes: a whole item to the output (or its half of the region), a part of one to a
+// slot of this worker (slot 1 if the item begins here, slot 0 if it goes on from an earlier
+// worker; a range holds at most one of each).
 __device__ __forceinline__ PagedDest paged_dest(const PagedShape &p, const PagedIO &io, int which,
                                                 bool begins, bool whole, int worker) {
   PagedDest d;

@@ -1,21 +1,21 @@
 // How the paged attention splits its work over a fixed grid.
 //
-// An item is the query heads of one kv head times up to `qt` consecutive tokens of a sequence, against
-// the key tiles they see; its cost is the number of those tiles plus a constant for starting and
-// storing it.  The costs of all items, ordered by (sequence, kv head, item, key tile), are cut into
-// equal ranges, one per worker, so the load is even whatever the lengths are: a batch of short and
-// long sequences, the triangle of a causal prompt, or one long context with a few rows.  An item cut
-// by a range boundary leaves one partial result per piece, and the pieces are joined afterwards in the
-// order of their keys.
-// There are three kinds of items, each with workers of its own: wide items (two query tiles that share
-// each key tile; a worker is a CTA), narrow ones (a sequence's last item if it has at most `qn` tokens:
-// one query tile; a worker is one of a CTA's two chains) and few-row ones (the last item if it has at
-// most `qf` tokens: single tokens and short tails; a worker is one of eight warps of a CTA).
-// Lengths live on the device, so each CTA derives the ranges of its workers itself: its threads share
-// the sequences out, and a warp per worker finds its sequence in a scan over their costs, then the item
-// within it.  All costs are 32-bit: a call whose sizes could pass 2^30 is refused on the host.  (In a
-// call for a single token this stands in the way of everything else, most of it the fetching of
-// instructions, so it is kept short: 64-bit costs and a search by one thread took 11 us.)
+// An item is the query heads of one kv head times up to `qt` consecutive tokens of a sequence,
+// against the key tiles they see; its cost is the number of those tiles plus a constant for
+// starting and storing it.  The costs of all items, ordered by (sequence, kv head, item, key
+// tile), are cut into equal ranges, one per worker, so the load is even whatever the lengths are:
+// a batch of short and long sequences, the triangle of a causal prompt, or one long context with a
+// few rows.  An item cut by a range boundary leaves one partial result per piece, and the pieces
+// are joined afterwards in the order of their keys. There are three kinds of items, each with
+// workers of its own: wide items (two query tiles that share each key tile; a worker is a CTA),
+// narrow ones (a sequence's last item if it has at most `qn` tokens: one query tile; a worker is
+// one of a CTA's two chains) and few-row ones (the last item if it has at most `qf` tokens: single
+// tokens and short tails; a worker is one of eight warps of a CTA). Lengths live on the device, so
+// each CTA derives the ranges of its workers itself: its threads share the sequences out, and a
+// warp per worker finds its sequence in a scan over their costs, then the item within it.  All
+// costs are 32-bit: a call whose sizes could pass 2^30 is refused on the host.  (In a call for a
+// single token this stands in the way of everything else, most of it the fetching of instructions,
+// so it is kept short: 64-bit costs and a search by one thread took 11 us.)
 #pragma once
 
 #include <stdint.h>
@@ -226,9 +226,10 @@ struct PagedScan {
   int error;
 };
 
-// Finds the ranges of this CTA's workers of the first KINDS kinds, with GROUP threads for each (thread t
-// works for kind t / GROUP; further threads take no part); warp j leaves the j-th worker's in start[j] and its head in heads[].  The block
-// synchronises inside, and has to before start is read.  Returns the largest error code of any sequence.
+// Finds the ranges of this CTA's workers of the first KINDS kinds, with GROUP threads for each
+// (thread t works for kind t / GROUP; further threads take no part); warp j leaves the j-th
+// worker's in start[j] and its head in heads[].  The block synchronises inside, and has to before
+// start is read.  Returns the largest error code of any sequence.
 template <int GROUP, int KINDS>
 __device__ __forceinline__ int paged_locate(const PagedShape &p, int cta, int ctas, int starts,
                                             PagedStart *start, PagedHead *heads, PagedScan &scan) {
@@ -308,9 +309,10 @@ __device__ __forceinline__ int paged_locate(const PagedShape &p, int cta, int ct
 }
 #endif
 
-// Walks the pieces of a worker's range in order: after begin(), while (more()), key tiles [t0, t1) of
-// item `item` (tokens [tok, tok + toks) of segment s, kv head `head`).  The starting cost of an item
-// lies before its first tile, and a range that ends within it leaves the item to the next worker.
+// Walks the pieces of a worker's range in order: after begin(), while (more()), key tiles [t0, t1)
+// of item `item` (tokens [tok, tok + toks) of segment s, kv head `head`).  The starting cost of an
+// item lies before its first tile, and a range that ends within it leaves the item to the next
+// worker.
 struct PagedWalk {
   PagedSeg s;
   int seg, head, index, items;        // index: among the items of the kind
@@ -366,8 +368,8 @@ struct PagedWalk {
   }
 };
 
-// The walk of few-row items alone: a segment has at most one, the same for every kv head, so that going
-// on costs a few operations and, at the end of a sequence's heads, the lengths of the next.
+// The walk of few-row items alone: a segment has at most one, the same for every kv head, so that
+// going on costs a few operations and, at the end of a sequence's heads, the lengths of the next.
 struct PagedFewWalk {
   int seq, head, seg, which;          // which: 0 the shared prefix, 1 the sequence's own keys
   int tok, toks;                      // packed rows [tok, tok + toks)
