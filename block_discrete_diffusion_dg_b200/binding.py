@@ -411,9 +411,11 @@ _ACT = {DG_F32: torch.float32, DG_BF16: torch.bfloat16}
 
 def _rows(t, name, dtype, *shape):
     """Pointer of a contiguous device tensor of this type that holds exactly `shape`."""
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: {dtype} {shape} wanted, {t.dtype} {tuple(t.shape)} given")
-    return _p(t)
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name}: the library takes contiguous device tensors")
+    return t.data_ptr()
 
 
 def _qkv_rows(cfg, qkv, rows):
@@ -440,9 +442,11 @@ def _pages(cfg, kv: PagedKV, n_seqs):
 
 
 def _index(t, name, n):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < n:
+    if t.dtype is not torch.int32 or t.ndim != 1 or t.numel() < n:
         raise ValueError(f"{name}: int32 of at least {n} wanted")
-    return _p(t)
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name}: the library takes contiguous device tensors")
+    return t.data_ptr()
 
 
 # The two lookups of a launch without the Python layers above them (4 us of a 14 us call).
