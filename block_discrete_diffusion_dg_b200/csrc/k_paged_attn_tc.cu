@@ -260,9 +260,9 @@ __global__ void __launch_bounds__(P_THR, 1)
     if (start[0].u1 > 0) {
       PagedWalk w;
       for (w.begin(p, PAGED_WIDE, start[0]); ok && w.more(); w.next(p)) {
+        int y = lookup(w, w.t0);   // (under way while the query tiles are asked for)
         load_q(w, 0, w.tok);
         if (ok) load_q(w, 1, w.tok + qn);
-        int y = lookup(w, w.t0);
         for (int t = w.t0; t < w.t1 && ok; ++t) {
           const int y_next = t + 1 < w.t1 ? lookup(w, t + 1) : -1;   // a tile ahead
           load(&tmK, w, t, y);
@@ -551,8 +551,8 @@ __global__ void __launch_bounds__(P_THR, 1)
         }
         fence_after();
         if (warp_on) {
-          const int worker = paged_first_worker(io, kind) +
-                             (kind == PAGED_WIDE ? 0 : x * io.ctas) + (int)blockIdx.x;
+          const int worker =
+              paged_first_worker(io, kind) + start[kind == PAGED_WIDE ? 0 : 1 + x].worker;
           const PagedDest dest = paged_dest(p, io, w, worker);
           const int on = min(32, rows - q4 * 32);       // rows of this warp
           const bool out = dest.kind == PAGED_OUT;
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(P_THR, 1)
           if (++t == t1) {   // the piece's result
             const FewPiece pc = pieces[np & 3];
             const int rows = pc.toks * rep, h0 = pc.head * rep;
-            const int worker = paged_first_worker(io, PAGED_FEW) + fw * io.ctas + blockIdx.x;
+            const int worker = paged_first_worker(io, PAGED_FEW) + few_start.worker;
             const PagedDest dest = paged_dest(p, io, pc.which, pc.t0 == 0, pc.whole, worker);
             const size_t base = paged_dest_base(p, io, dest);
 #pragma unroll

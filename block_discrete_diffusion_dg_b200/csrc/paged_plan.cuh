@@ -181,6 +181,7 @@ constexpr long long PAGED_COST_LIMIT = 1LL << 30;
 // A worker's place in the work of a kind: its range [u0, u1) of the total cost (u0 >= u1: none) and
 // the item that it begins in.
 struct PagedStart {
+  int worker;               // its number among those of the kind
   int u0, u1;
   int item_u0;              // where the item that holds u0 begins
   int per;                  // cost per worker
@@ -208,6 +209,34 @@ DG_HD PagedHead paged_head(const PagedShape &p, int kind, const PagedStart &st) 
     h.head = st.head;
   }
   return h;
+}
+
+// Shares the CTAs out among the kinds that have any cost: kind k gets CTAs [first[k], first[k] +
+// count[k]).  Where each CTA took its part of every kind one after the other it paid for a start per
+// kind (first loads, code not yet fetched), and the bytes of single tokens did not overlap the matrix
+// products of wide items: 128 single tokens over a shared prefix of 8192 keys took 61 us, now 49.
+// weight: cycles of a CTA per unit of cost on calls of one kind (wide: a key tile of both chains;
+// narrow: half of a tile of each chain; few-row: an eighth of 32 keys of each of eight warps, between
+// 300, right for many keys per token, and 500, right for a long prefix).
+DG_HD void paged_share(const int (&total)[3], int ctas, int (&first)[3], int (&count)[3]) {
+  constexpr float weight[3] = {3500.f, 1500.f, 400.f};
+  float t[3], sum = 0.f;
+  int big = 0;
+  for (int k = 0; k < 3; ++k) {
+    t[k] = (float)total[k] * weight[k];
+    sum += t[k];
+    if (t[k] > t[big]) big = k;
+  }
+  int rest = ctas;
+  for (int k = 0; k < 3; ++k) {
+    const int c = (int)((float)ctas * (t[k] / (sum > 0.f ? sum : 1.f)));
+    count[k] = k == big || total[k] == 0 ? 0 : c > 0 ? c : 1;
+    rest -= count[k];
+  }
+  count[big] = rest;
+  first[0] = 0;
+  first[1] = count[0];
+  first[2] = count[0] + count[1];
 }
 
 #ifdef __CUDACC__
@@ -259,14 +288,26 @@ __device__ __forceinline__ int paged_locate(const PagedShape &p, int cta, int ct
   const int j = tid >> 5;   // this warp's worker
   if (j < starts) {
     const int kind = j == 0 ? PAGED_WIDE : j < 3 ? PAGED_NARROW : PAGED_FEW;
-    // workers are dealt out over the CTAs, so that a small call uses many of them
-    const int n = paged_cta_workers(kind), worker = (j - paged_start_index(kind)) * ctas + cta;
+    int totals[3] = {0, 0, 0}, first[3], count[3];
+#pragma unroll
+    for (int k = 0; k < KINDS; ++k)
+      for (int w = 0; w < GROUP / 32; ++w) totals[k] += scan.sum[k][w];
+    paged_share(totals, ctas, first, count);
+    const int n = paged_cta_workers(kind), i = j - paged_start_index(kind);
+    const int mine_of = kind == 0 ? count[0] : kind == 1 ? count[1] : count[2];
+    const int begin = kind == 0 ? first[0] : kind == 1 ? first[1] : first[2];
+    const int total = kind == 0 ? totals[0] : kind == 1 ? totals[1] : totals[2];
+    const bool serves = cta >= begin && cta < begin + mine_of;
+    // workers are dealt out over the CTAs, so that a small call uses many of them; the numbers of
+    // CTAs that serve another kind come last
+    const int worker = serves ? i * mine_of + cta - begin
+                              : n * mine_of + i * (ctas - mine_of) + (cta < begin ? cta : cta - mine_of);
     PagedStart r{};
-    int total = 0;
-    for (int w = 0; w < GROUP / 32; ++w) total += scan.sum[kind][w];
-    r.per = (int)((uint32_t)(total + n * ctas - 1) / (uint32_t)(n * ctas));
+    r.worker = worker;
+    const uint32_t workers = n * (mine_of > 0 ? mine_of : 1);
+    r.per = (int)((uint32_t)(total + workers - 1) / workers);
     if (r.per < p.least[kind]) r.per = p.least[kind];
-    if (total > 0 && (uint32_t)worker * (uint32_t)r.per < (uint32_t)total) {
+    if (serves && total > 0 && (uint32_t)worker * (uint32_t)r.per < (uint32_t)total) {
       r.u0 = worker * r.per;
       r.u1 = r.u0 + r.per < total ? r.u0 + r.per : total;
       // the thread whose sequences hold u0: the last that begins at or before it

@@ -170,6 +170,19 @@ int main() {
       CHECK(at == all.size() && open < 0);
     }
   }
+  // the CTAs' shares: every kind with work has one at least, none overlap, all are given out
+  for (int t = 0; t < 20000; ++t) {
+    int total[3], first[3], count[3];
+    for (int k = 0; k < 3; ++k) total[k] = rnd(3) ? 0 : rnd(2) ? rnd(50) : rnd(1 << 30);
+    const int ctas = 3 + rnd(300);
+    paged_share(total, ctas, first, count);
+    int at = 0;
+    for (int k = 0; k < 3; ++k) {
+      CHECK(first[k] == at && count[k] >= (total[k] > 0));
+      at += count[k];
+    }
+    CHECK(at == ctas);
+  }
   // error codes
   int off[] = {0, 4, 2, 9, 12, 12}, kv[] = {5, 5, -1, 97, 1000000};
   PagedShape p{};
