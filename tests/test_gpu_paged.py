@@ -339,27 +339,105 @@ def test_pages_past_32_bit_offsets(n_new):
     assert P.worst(out, want, P.attention_bound(want, A, e, keys, torch.bfloat16, 2.0 ** -8)) <= 1.0
 
 
-@pytest.mark.parametrize("act,hq,hkv,hd", [("bf16", 16, 8, 128), ("f32", 4, 2, 64)])
-def test_extreme_scores(act, hq, hkv, hd):
-    """Scores far apart and growing along the keys: the running maximum moves on and late keys
-    take all of the weight; equal scores give the plain mean."""
+@pytest.mark.parametrize("act,hq,hkv,hd", [("bf16", 16, 8, 128), ("bf16", 8, 4, 64), ("f32", 4, 2, 64)])
+@pytest.mark.parametrize("n", [3, 40, 300])
+def test_extreme_scores(act, hq, hkv, hd, n):
+    """Scores far apart and growing along the keys: the running maximum moves on again and again and
+    late keys take all of the weight, or early ones do; equal scores give the plain mean.  For each
+    kind of work (n = 3, 40 and 300 rows of two heads)."""
     g = gen(5)
-    new, have = [3], [900]
-    c = Cache(g, act, hkv, hd, 64, [903])
+    new, have = [n], [900]
+    c = Cache(g, act, hkv, hd, 64, [900 + n])
     k, v = c.kept[0]
-    pos = torch.arange(903, device="cuda")
+    pos = torch.arange(900 + n, device="cuda")
     ids = c.table[0][pos // 64].long()
-    ramp = torch.linspace(-8, 8, 903, device="cuda")[:, None, None]
+    ramp = torch.linspace(-8, 8, 900 + n, device="cuda")[:, None, None]
     k = (torch.ones_like(k, dtype=torch.float32) * ramp).to(k.dtype)
     c.kept[0] = (k, v)
     c.k[ids, :, pos % 64] = k
-    q = torch.full((3, hq, hd), 2.0, device="cuda").to(DT[act])
-    q[1] = -2.0
-    q[2] = 0.0
+    q = torch.full((n, hq, hd), 2.0, device="cuda").to(DT[act])
+    q[1::3] = -2.0
+    q[2::3] = 0.0
     for causal in (0, 1):
         out, st = run_attention(make_cfg(act, hq, hkv, hd), c, new, have, q, causal)
         assert st == B.DG_OK
         check_attention(out, q, c, new, have, causal, act)
+
+
+@pytest.mark.parametrize("act,hq,hkv,hd", [("bf16", 16, 8, 128), ("f32", 4, 2, 64)])
+@pytest.mark.parametrize("shared", [0, 1024])
+def test_largest_page(act, hq, hkv, hd, shared):
+    g, new, own = gen(6), [1, 40, 300], [1500, 0, 1000]
+    have = [shared + o for o in own]
+    c = Cache(g, act, hkv, hd, 1024, [n + h for n, h in zip(new, have)], shared=shared)
+    q = (1.5 * randn(g, sum(new), hq, hd)).to(DT[act])
+    out, st = run_attention(make_cfg(act, hq, hkv, hd), c, new, have, q, 1, shared=shared)
+    assert st == B.DG_OK
+    check_attention(out, q, c, new, have, 1, act)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("shared", [0, 32])
+def test_empty_batches_and_rows_before_the_first(act, shared):
+    """Offsets that hold no row at all leave the output alone; rows before the first sequence are
+    nobody's, and stay too."""
+    g, hq, hkv, hd = gen(7), 4, 2, 64
+    cfg = make_cfg(act, hq, hkv, hd)
+    c = Cache(g, act, hkv, hd, 16, [shared + 40, shared + 90], shared=shared)
+    q = randn(g, 12, hq, hd).to(DT[act])
+    ws = B.alloc_paged_workspace(cfg, 2, 12, shared)
+    for off in ([0, 0, 0], [12, 12, 12], [3, 5, 9]):
+        ws.fill_(0xFF)
+        out, st = torch.full_like(q, MARK), i32([0])
+        have = [shared + 38, shared + 86]
+        args = (cfg, 2, 12, i32(off), i32(have)) + ((shared,) if shared else ())
+        (B.dg_prefix_attn if shared else B.dg_paged_attn)(*args, q, c.kv, 1, out, ws, st)
+        assert B.dg_read_status(st) == B.DG_OK
+        assert (out[:off[0]].float() == MARK).all() and (out[off[2]:].float() == MARK).all()
+        if off[0] == off[2]:
+            continue
+        check_attention(out[off[0]:], q[off[0]:], c, [2, 4], have, 1, act)
+        qkv = randn(g, 12, (hq + 2 * hkv) * hd).to(DT[act])
+        qo = torch.full_like(q, MARK)
+        B.dg_paged_append(cfg, 2, 12, i32(off), i32(have), qkv, None, None, B.make_rope(0), c.kv, qo, st)
+        assert B.dg_read_status(st) == B.DG_OK
+        assert torch.equal(qo[3:9], qkv[3:9, :hq * hd].view(6, hq, hd))
+        assert (qo[:3].float() == MARK).all() and (qo[9:].float() == MARK).all()
+
+
+def test_thousands_of_sequences():
+    g, hq, hkv, hd, seqs = gen(13), 4, 2, 64, 3000
+    rng = random.Random(4)
+    have = [rng.choice((0, 3, 20, 45)) for _ in range(seqs)]
+    new = [rng.choice((0, 1, 1, 1, 2)) for _ in range(seqs)]
+    c = Cache(g, "bf16", hkv, hd, 16, [n + h for n, h in zip(new, have)])
+    q = randn(g, sum(new), hq, hd).to(torch.bfloat16)
+    out, st = run_attention(make_cfg("bf16", hq, hkv, hd), c, new, have, q, 1)
+    assert st == B.DG_OK
+    check_attention(out, q, c, new, have, 1, "bf16")
+
+
+def test_calls_at_the_same_time():
+    """Two streams, each with its own workspace and sequences, over one cache: every result is the one
+    that the call gives alone."""
+    g, hq, hkv, hd = gen(17), 16, 8, 128
+    cfg = make_cfg("bf16", hq, hkv, hd)
+    new, have = [1, 1, 90, 300], [2000, 30, 500, 0]
+    c = Cache(g, "bf16", hkv, hd, 64, [n + h for n, h in zip(new, have)])
+    q = randn(g, sum(new), hq, hd).to(torch.bfloat16)
+    want = [run_attention(cfg, c, new, have, q, causal)[0] for causal in (0, 1)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [B.alloc_paged_workspace(cfg, 4, sum(new)) for _ in range(2)]
+    outs = [[torch.full_like(q, MARK) for _ in range(20)] for _ in range(2)]
+    off, lens = i32(offsets(new)), i32(have)
+    torch.cuda.synchronize()
+    for i in range(20):
+        for causal, s in enumerate(streams):
+            B.dg_paged_attn(cfg, 4, sum(new), off, lens, q, c.kv, causal, outs[causal][i], ws[causal],
+                            None, s)
+    torch.cuda.synchronize()
+    for causal in (0, 1):
+        assert all(torch.equal(o, want[causal]) for o in outs[causal])
 
 
 @pytest.mark.parametrize("act,hq,hkv,hd", [("bf16", 16, 8, 128), ("bf16", 8, 8, 64), ("f32", 4, 2, 64)])
@@ -516,6 +594,43 @@ def test_prompt_then_tokens_then_canvases(act, hq, hkv, hd):
         step([1 if rng.random() < 0.8 else 0 for _ in range(forks)], 1, prompt)
     step([canvas] * forks, 0, prompt)
     step([1] * forks, 1, 0)
+
+
+def test_captured_step_over_a_shared_prefix():
+    """An append and a shared-prefix attention captured together, replayed as the sequences grow."""
+    g, hq, hkv, hd, page, shared, seqs = gen(33), 16, 8, 128, 16, 64, 6
+    cfg = make_cfg("bf16", hq, hkv, hd)
+    c = Cache(g, "bf16", hkv, hd, page, [shared + 60] * seqs, shared=shared)
+    for s in range(seqs):                                # only the prefix is there yet
+        ids = c.table[s, shared // page:shared // page + 4].long()
+        c.k[ids] = math.nan
+        c.v[ids] = math.nan
+    keys = [[k[:shared].clone(), v[:shared].clone()] for k, v in c.kept]
+    rows = 24
+    qkv = torch.zeros(rows, (hq + 2 * hkv) * hd, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(rows, hq, hd, dtype=torch.bfloat16, device="cuda")
+    out, off, lens, st = torch.empty_like(q), i32([0] * (seqs + 1)), i32([shared] * seqs), i32([0])
+    ws = B.alloc_paged_workspace(cfg, seqs, rows, shared)
+    rope = B.make_rope(0)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        B.dg_paged_append(cfg, seqs, rows, off, lens, qkv, None, None, rope, c.kv, q, st)
+        B.dg_prefix_attn(cfg, seqs, rows, off, lens, shared, q, c.kv, 1, out, ws, st)
+    have = [shared] * seqs
+    for new in ([1] * 6, [0, 10, 1, 0, 9, 4], [1, 1, 0, 1, 1, 1], [0] * 6, [2, 0, 3, 1, 0, 5]):
+        qkv.copy_(randn(g, *qkv.shape).to(torch.bfloat16))
+        off.copy_(i32(offsets(new)))
+        lens.copy_(i32(have))
+        out.fill_(MARK)
+        gr.replay()
+        assert B.dg_read_status(st) == B.DG_OK
+        x = qkv.view(rows, hq + 2 * hkv, hd)
+        for s, (a, n) in enumerate(zip(offsets(new), new)):
+            keys[s][0] = torch.cat((keys[s][0], x[a:a + n, hq:hq + hkv]))
+            keys[s][1] = torch.cat((keys[s][1], x[a:a + n, hq + hkv:]))
+        c.kept = [tuple(kv) for kv in keys]
+        check_attention(out, x[:, :hq].contiguous(), c, new, have, 1, "bf16")
+        have = [h + n for h, n in zip(have, new)]
 
 
 def test_captured_calls_follow_their_buffers():

@@ -84,13 +84,13 @@ def test_append_and_norm_refusals():
     n0 = B.dg_launch_count()
     cfg, kv, rope = _cfg(), _kv(), B.make_rope(128)
     for i, v in ((0, 0), (1, 0), (2, None), (3, None), (4, None), (4, 264), (5, 4088), (5, 4100),
-                 (9, None), (10, 264)):
+                 (6, 264), (7, 264), (9, None), (10, 264)):
         a = _append_args(kv, rope)
         a[i] = v
         assert _call("dg_paged_append", cfg, a) == B.DG_ERR_INVALID_ARG, (i, v)
     for bad in BAD_PAGES:
         assert _call("dg_paged_append", cfg, _append_args(_kv(**bad), rope)) == B.DG_ERR_INVALID_ARG
-    for i, v in ((0, 0), (1, 0), (2, None), (2, 264), (3, 4088), (3, 4100), (4, None), (8, None),
+    for i, v in ((0, 0), (1, 0), (2, None), (2, 264), (3, 4088), (3, 4100), (4, None), (5, 264), (6, 264), (8, None),
                  (9, None), (9, 264), (10, None)):
         a = _norm_args(rope)
         a[i] = v
