@@ -500,7 +500,9 @@ __global__ void __launch_bounds__(P_THR, 1)
             // O is rescaled only when a row's maximum grew by more than 2^8 (P stays below 256, and
             // O and l share their base, so O / l does not change); S of this tile was issued behind
             // the last P V, so O includes it
-            if (__any_sync(FULL, m_use != -INFINITY && m_new > m_use + P_RESCALE)) {
+            // (rows past the item's last hold another's, or what was in shared memory: not asked, so
+            // that results do not depend on them)
+            if (__any_sync(FULL, r < rows && m_use != -INFINITY && m_new > m_use + P_RESCALE)) {
               const float g = m_use == -INFINITY ? 1.f : ex2(m_use - m_new);
 #pragma unroll 1
               for (int c = 0; c < HD / 32; ++c) {

@@ -498,6 +498,41 @@ def test_bad_page_ids_are_reported():
         c.kept[1] = keep
 
 
+@pytest.mark.parametrize("hq,hkv", [(6, 2), (5, 1), (14, 2)])
+def test_results_do_not_hang_on_the_call_before(hq, hkv):
+    """Groups that do not divide a query tile leave rows of it to whatever another call left in shared
+    memory; a sequence's neighbours stand in the rows behind its own.  Neither may show in a result."""
+    g, hd, n, have = gen(18), 128, 128 // (hq // hkv), 4000
+    cfg = make_cfg("bf16", hq, hkv, hd)
+    c = Cache(g, "bf16", hkv, hd, 64, [have + n])
+    ramp = torch.linspace(0, 1, have + n, device="cuda")[:, None, None]
+    k = (ramp + 0.02 * randn(g, have + n, hkv, hd)).to(torch.bfloat16)
+    v = c.kept[0][1]
+    pos = torch.arange(have + n, device="cuda")
+    c.k[c.table[0][pos // 64].long(), :, pos % 64] = k
+    c.kept[0] = (k, v)
+    # the same sequence many times over, so that items stay whole and pass many key tiles
+    seqs = 300
+    many = B.PagedKV(c.k, c.v, c.table.repeat(seqs, 1))
+    off, lens = i32([i * n for i in range(seqs + 1)]), i32([have] * seqs)
+    wide_ws = B.alloc_paged_workspace(cfg, seqs, seqs * n)
+    q = (0.2 + 0.02 * randn(g, n, hq, hd)).to(torch.bfloat16)
+    qs = q.repeat(seqs, 1, 1)
+    big = make_cfg("bf16", 2 * hkv, 2 * hkv, hd)
+    pages = torch.ones(2, 2 * hkv, 64, hd, dtype=torch.bfloat16, device="cuda")
+    kv = B.PagedKV(pages, pages, torch.zeros(148, 2, dtype=torch.int32, device="cuda"))
+    ws = B.alloc_paged_workspace(big, 148, 148 * 100)
+    outs = []
+    for value in (0.0, 100.0, -3.0):
+        qb = torch.full((148 * 100, 2 * hkv, hd), value, dtype=torch.bfloat16, device="cuda")
+        B.dg_paged_attn(big, 148, 148 * 100, i32([100 * i for i in range(149)]), i32([0] * 148), qb, kv,
+                        0, torch.empty_like(qb), ws)
+        outs.append(torch.empty_like(qs))
+        B.dg_paged_attn(cfg, seqs, seqs * n, off, lens, qs, many, 0, outs[-1], wide_ws)
+    check_attention(outs[0][:n], q, c, [n], [have], 0, "bf16")
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
 # ----------------------------------------------------------------------------------- as used
 
 def test_matches_canvas_attention():
