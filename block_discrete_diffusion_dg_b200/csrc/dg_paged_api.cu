@@ -90,7 +90,7 @@ PagedCall paged_call(const dg_config *cfg, int n_seqs, int n_tokens, int shared_
 }
 
 bool sizes_ok(const dg_config *cfg, int n_seqs, int n_tokens) {
-  return cfg_ok(cfg) && n_seqs > 0 && n_tokens > 0 &&
+  return cfg_ok(cfg) && n_seqs > 0 && n_seqs < (1 << 30) && n_tokens > 0 &&
          (long long)n_tokens * cfg->n_q_heads <= INT32_MAX;
 }
 

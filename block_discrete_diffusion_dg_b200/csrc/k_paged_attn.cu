@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_con
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       ml[i][k] = io.part_ml[paged_region_row(p, io, k, tok, min(h0 + i, io.Hq - 1))];
+  if (io.heads[0].refused) return;   // (the region was not written)
   // the sequence that holds this row, if it is one the attention took
   int lo = 0, hi = p.n_seqs;
   while (hi - lo > 1) {

@@ -112,10 +112,7 @@ __device__ __forceinline__ TokenSpot packed_spot(const QkvArgs &a, int t, int *p
   }
   const int o0 = a.seq_off[lo], o1 = a.seq_off[lo + 1], have = a.len[lo];
   if (o0 > t || t >= o1) return sp;   // no sequence's row
-  if (o0 < 0 || o1 > a.n_tokens || have < 0) {
-    if (lane == 0) set_status(a.status, DG_ERR_INVALID_ARG);
-    return sp;
-  }
+  if (o0 < 0 || o1 > a.n_tokens || have < 0) return sp;   // (recorded by the thread that checks it)
   sp.row = t;
   // (a position past 2^31 is past every cache: its q is rotated by the wrapped position)
   const int pos = (int)((uint32_t)have + (uint32_t)(t - o0));
@@ -161,6 +158,17 @@ __global__ void __launch_bounds__(Q_THR) qkv_rows_kernel(const __grid_constant__
   if (slot < work) {
     A.load(src + ca * 8);
     B.load(src + cb * 8);
+  }
+  // Sequences that no row reaches are checked too, a thread each, from the warps that have no token in
+  // a small call.
+  if (a.n == 0) {
+#pragma unroll 1
+    for (long long s = (long long)blockIdx.x * Q_THR + Q_THR - 1 - tid; s < a.n_seqs;
+         s += (long long)gridDim.x * Q_THR) {
+      const int o0 = a.seq_off[s], o1 = a.seq_off[s + 1];
+      if (o0 != o1 && (o0 < 0 || o1 < o0 || o1 > a.n_tokens || a.len[s] < 0))
+        set_status(a.status, DG_ERR_INVALID_ARG);
+    }
   }
   {
     // a warp per token

@@ -54,6 +54,9 @@ struct PagedSeg {
   int seq;                  // page-table row
   int error;                // 0, 1: malformed offsets or lengths, 2: keys past the page table
 };
+// Error of a whole call: offsets that descend.  What the costs add up to is only bounded, and a row
+// only in one sequence, where they ascend, so nothing is attended then.
+constexpr int PAGED_DESCENDS = 3;
 
 DG_HD int paged_segs(const PagedShape &p) { return p.n_seqs + (p.shared_len > 0 ? 1 : 0); }
 
@@ -92,6 +95,12 @@ DG_HD PagedSeg paged_seg(const PagedShape &p, int index) {
     s.keys = have - p.shared_len + s.n;
   }
   return s;
+}
+
+// Error of the call that segment `index`, found malformed, stands for.
+DG_HD int paged_error(const PagedShape &p, int index, int error) {
+  const int i = p.shared_len > 0 ? index - 1 : index;   // (the prefix has no error)
+  return p.seq_off[i + 1] < p.seq_off[i] ? PAGED_DESCENDS : error;
 }
 
 // sum_{i < n} floor((a i + b) / m) for a, b >= 0, m > 0 (each term and the sum below 2^31).
@@ -194,10 +203,11 @@ struct PagedHead {
   int first, last;          // workers (of the kind) that hold its first and last tile; first < 0: the
                             // range does not begin inside an item
   int tok0, tokens, head;   // packed rows and kv head of the item
-  int pad[3];
+  int refused;              // nothing is attended (the same in every worker's)
+  int pad[2];
 };
 DG_HD PagedHead paged_head(const PagedShape &p, int kind, const PagedStart &st) {
-  PagedHead h = {-1, 0, 0, 0, 0, {0, 0, 0}};
+  PagedHead h = {-1, 0, 0, 0, 0, 0, {0, 0}};
   const int c = p.start_cost[kind];
   if (st.u0 < st.u1 && st.u0 - st.item_u0 > c) {
     const int item = paged_first_item(p, st.s, kind) + st.item;
@@ -269,29 +279,30 @@ __device__ __forceinline__ int paged_locate(const PagedShape &p, int cta, int ct
   __syncthreads();
   if (tid < KINDS * GROUP) {
     const int kind = tid / GROUP, t = tid % GROUP;
-    int mine = 0;   // cost of this thread's sequences
+    uint32_t mine = 0;   // cost of this thread's sequences (past 32 bits only where offsets descend)
     for (int i = t * chunk; i < min((t + 1) * chunk, segs); ++i) {
       const PagedSeg s = paged_seg(p, i);
-      if (s.error) atomicMax(&scan.error, s.error);
-      mine += p.Hkv * paged_head_cost(p, s, kind);
+      if (s.error) atomicMax(&scan.error, paged_error(p, i, s.error));
+      mine += (uint32_t)p.Hkv * (uint32_t)paged_head_cost(p, s, kind);
     }
-    int inc = mine;
+    uint32_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(full, inc, o);
+      const uint32_t v = __shfl_up_sync(full, inc, o);
       if (lane >= o) inc += v;
     }
-    scan.before[kind][t] = inc - mine;
-    if (lane == 31) scan.sum[kind][t >> 5] = inc;
+    scan.before[kind][t] = (int)(inc - mine);
+    if (lane == 31) scan.sum[kind][t >> 5] = (int)inc;
   }
   __syncthreads();
   const int j = tid >> 5;   // this warp's worker
   if (j < starts) {
     const int kind = j == 0 ? PAGED_WIDE : j < 3 ? PAGED_NARROW : PAGED_FEW;
+    const bool refused = scan.error == PAGED_DESCENDS;
     int totals[3] = {0, 0, 0}, first[3], count[3];
 #pragma unroll
     for (int k = 0; k < KINDS; ++k)
-      for (int w = 0; w < GROUP / 32; ++w) totals[k] += scan.sum[k][w];
+      for (int w = 0; w < GROUP / 32; ++w) totals[k] += refused ? 0 : scan.sum[k][w];
     paged_share(totals, ctas, first, count);
     const int n = paged_cta_workers(kind), i = j - paged_start_index(kind);
     const int mine_of = kind == 0 ? count[0] : kind == 1 ? count[1] : count[2];
@@ -342,8 +353,9 @@ __device__ __forceinline__ int paged_locate(const PagedShape &p, int cta, int ct
     }
     if (lane == 0) {
       start[j] = r;
-      heads[(kind == PAGED_WIDE ? 0 : kind == PAGED_NARROW ? ctas : 3 * ctas) + worker] =
-          paged_head(p, kind, r);
+      PagedHead h = paged_head(p, kind, r);
+      h.refused = refused;
+      heads[(kind == PAGED_WIDE ? 0 : kind == PAGED_NARROW ? ctas : 3 * ctas) + worker] = h;
     }
   }
   return scan.error;

@@ -400,9 +400,11 @@ int dg_generate(const dg_config *cfg, const dg_model *model, int batch, int32_t 
  * Errors the device sees: offsets or lengths that are negative, not ascending or past n_tokens, and
  *   page ids outside [0, n_pages), record DG_ERR_INVALID_ARG; a sequence whose keys would pass
  *   max_pages * page_size records DG_ERR_CAPACITY.  Such a sequence is skipped (its output rows and
- *   pages are left as they were), except that a bad page id among an attention's keys leaves that
+ *   pages are left as they were); where offsets descend, the attention calls leave every row as it
+ *   was, and the append serves a row for one of the sequences that claim it.  But a bad page id among an attention's keys leaves that
  *   sequence's output rows (with a shared prefix, if the page is one of the prefix: every row)
- *   without meaning.  Nothing is read or written out of range. */
+ *   without meaning.  Nothing is read or written out of range.
+ * A workspace serves one call at a time: calls that may run at once take one each. */
 
 /* One layer's pages (HOST struct).  Key j of sequence s is row j % page_size of page
  * page_table[s][j / page_size]; entries behind a sequence's last key are not read.  What stands
@@ -451,7 +453,8 @@ int dg_qk_norm_rope(const dg_config *cfg, int batch, int n_tokens, const void *q
 
 /* The same for packed rows, with K and V written straight to their pages: row i of sequence s goes
  * to key kv_len[s] + i.  q [n_tokens][Hq][hd], or NULL where only the cache is filled.  A sequence
- * that does not fit its pages, or a row whose page id is bad, still gets its q. */
+ * that does not fit its pages, or a row whose page id is bad, still gets its q.  Pages may be shared
+ * between sequences, but not those that new tokens go to (which of two rows stays is not defined). */
 int dg_paged_append(const dg_config *cfg, int n_seqs, int n_tokens, const int32_t *seq_off,
                     const int32_t *kv_len, const void *qkv, long long ld_qkv, const float *q_gain,
                     const float *k_gain, const dg_rope *rope, const dg_paged_kv *kv, void *q,

@@ -498,6 +498,62 @@ def test_bad_page_ids_are_reported():
         c.kept[1] = keep
 
 
+@pytest.mark.parametrize("act,hq,hkv,hd", [("bf16", 16, 8, 128), ("f32", 4, 2, 64)])
+@pytest.mark.parametrize("off", [[0, 10, 5, 12], [0, 12, 4], [0, 3, 3, 12, -2], [4, 4, 2]])
+def test_descending_offsets_attend_nothing(act, hq, hkv, hd, off):
+    """Where offsets descend no row is written, whatever a workspace holds, and every call reports."""
+    g, n, seqs, cfg = gen(14), 12, len(off) - 1, make_cfg(act, hq, hkv, hd)
+    c = Cache(g, act, hkv, hd, 16, [32 + 40] * seqs, shared=32)
+    q = randn(g, n, hq, hd).to(DT[act])
+    have, st = [32 + 20] * seqs, i32([0])
+    for shared in (0, 32):
+        ws = B.alloc_paged_workspace(cfg, seqs, n, shared)
+        for fill in (0, 0x7F, 0xBF):
+            ws.fill_(fill)
+            out = torch.full_like(q, MARK)
+            args = (cfg, seqs, n, i32(off), i32(have)) + ((shared,) if shared else ())
+            (B.dg_prefix_attn if shared else B.dg_paged_attn)(*args, q, c.kv, 1, out, ws, st)
+            assert B.dg_read_status(st) == B.DG_ERR_INVALID_ARG
+            B.dg_clear_status(st)
+            assert (out.float() == MARK).all()
+    B.dg_paged_append(cfg, seqs, n, i32(off), i32(have), randn(g, n, (hq + 2 * hkv) * hd).to(DT[act]),
+                      None, None, B.make_rope(0), c.kv, q, st)
+    assert B.dg_read_status(st) == B.DG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("act,hq,hkv,hd", [("bf16", 16, 8, 128), ("f32", 4, 4, 32)])
+def test_sequences_that_claim_the_same_rows(act, hq, hkv, hd):
+    """Offsets that go back and forth: thousands of sequences of 40,000 rows each, whose work adds up
+    past 32 bits, are refused as a whole."""
+    n, seqs, have = 40000, 8001, 25000
+    off = i32([0, n] * (seqs // 2 + 1))
+    pages = torch.zeros(2, hkv, 1024, hd, dtype=DT[act], device="cuda")
+    kv = B.PagedKV(pages, pages, torch.zeros(seqs, 64, dtype=torch.int32, device="cuda"))
+    q = torch.zeros(n, hq, hd, dtype=DT[act], device="cuda")
+    out, st, cfg = torch.full_like(q, MARK), i32([0]), make_cfg(act, hq, hkv, hd)
+    for shared in (0, 1024):
+        ws = B.alloc_paged_workspace(cfg, seqs, n, shared)
+        args = (cfg, seqs, n, off, i32([have] * seqs)) + ((shared,) if shared else ())
+        (B.dg_prefix_attn if shared else B.dg_paged_attn)(*args, q, kv, 1, out, ws, st)
+        assert B.dg_read_status(st) == B.DG_ERR_INVALID_ARG
+        B.dg_clear_status(st)
+        assert (out.float() == MARK).all()
+
+
+@pytest.mark.parametrize("off,lens,code", [
+    ([20, 30], [5], B.DG_ERR_INVALID_ARG), ([0, 30], [5], B.DG_ERR_INVALID_ARG),
+    ([-3, 4], [5], B.DG_ERR_INVALID_ARG), ([0, 4, 8], [5, -1], B.DG_ERR_INVALID_ARG),
+    ([0, 4, 8], [5, 1000], B.DG_ERR_CAPACITY), ([0, 4, 4], [5, -1], B.DG_OK),
+    ([0, 2, 4, 8, 6], [5] * 4, B.DG_ERR_INVALID_ARG)])
+def test_append_reports_what_the_attention_reports(off, lens, code):
+    g, n, cfg = gen(15), 8, make_cfg("bf16", 4, 2, 64)
+    c = Cache(g, "bf16", 2, 64, 16, [60] * len(lens))
+    q, st = torch.empty(n, 4, 64, dtype=torch.bfloat16, device="cuda"), i32([0])
+    B.dg_paged_append(cfg, len(lens), n, i32(off), i32(lens), randn(g, n, 8 * 64).to(torch.bfloat16),
+                      None, None, None, c.kv, q, st)
+    assert B.dg_read_status(st) == code
+
+
 @pytest.mark.parametrize("hq,hkv", [(6, 2), (5, 1), (14, 2)])
 def test_results_do_not_hang_on_the_call_before(hq, hkv):
     """Groups that do not divide a query tile leave rows of it to whatever another call left in shared
