@@ -179,9 +179,11 @@ __global__ void __launch_bounds__(Q_THR) qkv_rows_kernel(const __grid_constant__
       int pos = 0;
       if (a.n > 0) {
         const int b = t / a.n, i = t % a.n;
-        sp.row = t;
-        sp.kv_row = (long long)b * a.Hkv * a.n + i;
-        pos = a.len[b] + i;
+        const int have = a.len[b];
+        sp.row = have < 0 ? -1 : t;
+        sp.kv_row = have < 0 ? -1 : (long long)b * a.Hkv * a.n + i;
+        if (have < 0 && (tid & 31) == 0) set_status(a.status, DG_ERR_INVALID_ARG);
+        pos = (int)((uint32_t)have + (uint32_t)i);
       } else {
         sp = packed_spot(a, t, &pos);
       }

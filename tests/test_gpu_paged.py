@@ -554,6 +554,28 @@ def test_append_reports_what_the_attention_reports(off, lens, code):
     assert B.dg_read_status(st) == code
 
 
+def test_norm_reports_negative_lengths():
+    """A canvas of negative length is skipped, the others come out as ever."""
+    g, n, hq, hkv, hd = gen(16), 20, 4, 2, 64
+    cfg = make_cfg("bf16", hq, hkv, hd)
+    qkv = randn(g, 3 * n, (hq + 2 * hkv) * hd).to(torch.bfloat16)
+
+    def run(lens):
+        q = torch.full((3, n, hq, hd), MARK, dtype=torch.bfloat16, device="cuda")
+        k = torch.full((3, hkv, n, hd), MARK, dtype=torch.bfloat16, device="cuda")
+        v, st = torch.full_like(k, MARK), i32([0])
+        B.dg_qk_norm_rope(cfg, 3, n, qkv, i32(lens), None, None, None, q, k, v, st)
+        return (q, k, v), B.dg_read_status(st)
+
+    want, st = run([4, 8, 9])
+    assert st == B.DG_OK
+    got, st = run([4, -8, 9])
+    assert st == B.DG_ERR_INVALID_ARG
+    for w, t in zip(want, got):
+        assert torch.equal(t[0], w[0]) and torch.equal(t[2], w[2])
+        assert (t[1].float() == MARK).all()
+
+
 @pytest.mark.parametrize("hq,hkv", [(6, 2), (5, 1), (14, 2)])
 def test_results_do_not_hang_on_the_call_before(hq, hkv):
     """Groups that do not divide a query tile leave rows of it to whatever another call left in shared
