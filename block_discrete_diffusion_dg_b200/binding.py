@@ -398,9 +398,11 @@ class PagedKV:
             raise ValueError("k_pages and v_pages are alike, [n_pages][Hkv][page][hd]")
         if page_table.dim() != 2 or page_table.dtype != torch.int32:
             raise ValueError("the page table is int32 [n_seqs][max_pages]")
+        if not k_pages.device == v_pages.device == page_table.device:
+            raise ValueError("pages and page table on different devices")
         self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
         self.act, self.kv_heads, self.head_dim = k_pages.dtype, k_pages.shape[1], k_pages.shape[3]
-        self.seqs = page_table.shape[0]
+        self.seqs, self.dev = page_table.shape[0], k_pages.get_device()
         self.struct = DgPagedKv(_p(k_pages), _p(v_pages), _p(page_table), k_pages.shape[0],
                                 k_pages.shape[2], page_table.shape[1])
         self.ref = ctypes.byref(self.struct)
@@ -409,44 +411,64 @@ class PagedKV:
 _ACT = {DG_F32: torch.float32, DG_BF16: torch.bfloat16}
 
 
-def _rows(t, name, dtype, *shape):
+def _there(t, name, dev):
+    """Refuses a tensor that is not on device `dev` (None: on any), or not contiguous."""
+    here = t.get_device()
+    if here < 0 or not t.is_contiguous():
+        raise ValueError(f"{name}: the library takes contiguous device tensors")
+    if dev is not None and here != dev:
+        raise ValueError(f"{name}: on device {here}, the call's rows are on {dev}")
+
+
+def _rows(t, name, dtype, *shape, dev=None):
     """Pointer of a contiguous device tensor of this type that holds exactly `shape`."""
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: {dtype} {shape} wanted, {t.dtype} {tuple(t.shape)} given")
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name}: the library takes contiguous device tensors")
+    _there(t, name, dev)
     return t.data_ptr()
 
 
 def _qkv_rows(cfg, qkv, rows):
-    """Pointer and row stride of projected rows [rows][(Hq + 2 Hkv) hd]; the rows may lie apart."""
+    """Pointer, row stride and device of projected rows [rows][(Hq + 2 Hkv) hd]; the rows may lie
+    apart."""
     width = (cfg.n_q_heads + 2 * cfg.n_kv_heads) * cfg.head_dim
     if qkv.dtype != _ACT[cfg.act_dtype] or qkv.shape != (rows, width):
         raise ValueError(f"qkv: {_ACT[cfg.act_dtype]} {(rows, width)} wanted, "
                          f"{qkv.dtype} {tuple(qkv.shape)} given")
-    if not qkv.is_cuda or qkv.stride(1) != 1:
+    dev = qkv.get_device()
+    if dev < 0 or qkv.stride(1) != 1:
         raise ValueError("qkv: device rows of contiguous elements wanted")
-    return qkv.data_ptr(), (qkv.stride(0) if rows > 1 else width)
+    return qkv.data_ptr(), (qkv.stride(0) if rows > 1 else width), dev
 
 
-def _gain(cfg, g, name):
-    return None if g is None else _rows(g, name, torch.float32, cfg.head_dim)
+def _gain(cfg, g, name, dev):
+    return None if g is None else _rows(g, name, torch.float32, cfg.head_dim, dev=dev)
 
 
-def _pages(cfg, kv: PagedKV, n_seqs):
+def _pages(cfg, kv: PagedKV, n_seqs, dev):
     if kv.act != _ACT[cfg.act_dtype] or kv.kv_heads != cfg.n_kv_heads or kv.head_dim != cfg.head_dim:
         raise ValueError("the pages do not fit the config")
     if kv.seqs < n_seqs:
         raise ValueError("the page table has fewer rows than there are sequences")
+    if kv.dev != dev:
+        raise ValueError(f"pages on device {kv.dev}, the call's rows are on {dev}")
     return kv.ref
 
 
-def _index(t, name, n):
+def _index(t, name, n, dev=None):
     if t.dtype is not torch.int32 or t.ndim != 1 or t.numel() < n:
         raise ValueError(f"{name}: int32 of at least {n} wanted")
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name}: the library takes contiguous device tensors")
+    _there(t, name, dev)
     return t.data_ptr()
+
+
+def _status(t, dev):
+    return None if t is None else _index(t, "dev_status", 1, dev)
+
+
+def _scratch(ws, dev):
+    _there(ws, "ws", dev)
+    return _ws(ws)
 
 
 # The two lookups of a launch without the Python layers above them (4 us of a 14 us call).
@@ -455,16 +477,15 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _launch(name, device, stream, *args):
+def _launch(name, dev, stream, *args):
     """The library's `name`(*args, stream) on the tensors' device, which need not be the current
     one; stream None: that device's current stream."""
     fn = getattr(_lib or lib(), name)
-    index = device.index
-    s = _raw_stream(index) if stream is None else _stream(stream)
-    if index == _current_device():
+    s = _raw_stream(dev) if stream is None else _stream(stream)
+    if dev == _current_device():
         rc = fn(*args, s)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             rc = fn(*args, s)
     if rc != DG_OK:
         raise DgError(rc, name)
@@ -473,26 +494,26 @@ def _launch(name, device, stream, *args):
 def dg_qk_norm_rope(cfg, batch, n_tokens, qkv, cache_len, q_gain, k_gain, rope: Optional[DgRope], q,
                     k_new, v_new, dev_status=None, stream=None):
     """Per-head norms, rotation and head split of projected rows (ready for dg_canvas_attn)."""
-    ptr, ld = _qkv_rows(cfg, qkv, batch * n_tokens)
+    ptr, ld, dev = _qkv_rows(cfg, qkv, batch * n_tokens)
     act, hd, hkv = _ACT[cfg.act_dtype], cfg.head_dim, cfg.n_kv_heads
-    _launch("dg_qk_norm_rope", qkv.device, stream, ctypes.byref(cfg), batch,
-            n_tokens, ptr, ld, _index(cache_len, "cache_len", batch), _gain(cfg, q_gain, "q_gain"),
-            _gain(cfg, k_gain, "k_gain"), None if rope is None else ctypes.byref(rope),
-            _rows(q, "q", act, batch, n_tokens, cfg.n_q_heads, hd),
-            _rows(k_new, "k_new", act, batch, hkv, n_tokens, hd),
-            _rows(v_new, "v_new", act, batch, hkv, n_tokens, hd), _p(dev_status))
+    _launch("dg_qk_norm_rope", dev, stream, ctypes.byref(cfg), batch, n_tokens, ptr, ld,
+            _index(cache_len, "cache_len", batch, dev), _gain(cfg, q_gain, "q_gain", dev),
+            _gain(cfg, k_gain, "k_gain", dev), None if rope is None else ctypes.byref(rope),
+            _rows(q, "q", act, batch, n_tokens, cfg.n_q_heads, hd, dev=dev),
+            _rows(k_new, "k_new", act, batch, hkv, n_tokens, hd, dev=dev),
+            _rows(v_new, "v_new", act, batch, hkv, n_tokens, hd, dev=dev), _status(dev_status, dev))
 
 
 def dg_paged_append(cfg, n_seqs, n_tokens, seq_off, kv_len, qkv, q_gain, k_gain,
                     rope: Optional[DgRope], kv: PagedKV, q, dev_status=None, stream=None):
     """Per-head norms and rotation of packed rows; q packed, K and V into their pages."""
-    ptr, ld = _qkv_rows(cfg, qkv, n_tokens)
-    _launch("dg_paged_append", qkv.device, stream, ctypes.byref(cfg), n_seqs,
-            n_tokens, _index(seq_off, "seq_off", n_seqs + 1), _index(kv_len, "kv_len", n_seqs), ptr,
-            ld, _gain(cfg, q_gain, "q_gain"), _gain(cfg, k_gain, "k_gain"),
-            None if rope is None else ctypes.byref(rope), _pages(cfg, kv, n_seqs),
+    ptr, ld, dev = _qkv_rows(cfg, qkv, n_tokens)
+    _launch("dg_paged_append", dev, stream, ctypes.byref(cfg), n_seqs, n_tokens,
+            _index(seq_off, "seq_off", n_seqs + 1, dev), _index(kv_len, "kv_len", n_seqs, dev), ptr,
+            ld, _gain(cfg, q_gain, "q_gain", dev), _gain(cfg, k_gain, "k_gain", dev),
+            None if rope is None else ctypes.byref(rope), _pages(cfg, kv, n_seqs, dev),
             None if q is None else _rows(q, "q", _ACT[cfg.act_dtype], n_tokens, cfg.n_q_heads,
-                                         cfg.head_dim), _p(dev_status))
+                                         cfg.head_dim, dev=dev), _status(dev_status, dev))
 
 
 def dg_paged_workspace_size(cfg, n_seqs, n_tokens, shared_len=0) -> int:
@@ -509,23 +530,26 @@ def alloc_paged_workspace(cfg, n_seqs, n_tokens, shared_len=0, device="cuda"):
 def dg_paged_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, q, kv: PagedKV, causal, out, ws,
                   dev_status=None, stream=None):
     """Attention of packed sequences over their pages (the new K and V already appended)."""
-    w, wb = _ws(ws)
+    dev = q.get_device()
+    w, wb = _scratch(ws, dev)
     act, hq, hd = _ACT[cfg.act_dtype], cfg.n_q_heads, cfg.head_dim
-    _launch("dg_paged_attn", q.device, stream, ctypes.byref(cfg), n_seqs,
-            n_tokens, _index(seq_off, "seq_off", n_seqs + 1), _index(kv_len, "kv_len", n_seqs),
-            _rows(q, "q", act, n_tokens, hq, hd), _pages(cfg, kv, n_seqs), 1 if causal else 0,
-            _rows(out, "out", act, n_tokens, hq, hd), w, wb, _p(dev_status))
+    _launch("dg_paged_attn", dev, stream, ctypes.byref(cfg), n_seqs, n_tokens,
+            _index(seq_off, "seq_off", n_seqs + 1, dev), _index(kv_len, "kv_len", n_seqs, dev),
+            _rows(q, "q", act, n_tokens, hq, hd), _pages(cfg, kv, n_seqs, dev), 1 if causal else 0,
+            _rows(out, "out", act, n_tokens, hq, hd, dev=dev), w, wb, _status(dev_status, dev))
 
 
 def dg_prefix_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, shared_len, q, kv: PagedKV, causal, out,
                    ws, dev_status=None, stream=None):
     """dg_paged_attn where the first shared_len keys are common to all sequences, read once."""
-    w, wb = _ws(ws)
+    dev = q.get_device()
+    w, wb = _scratch(ws, dev)
     act, hq, hd = _ACT[cfg.act_dtype], cfg.n_q_heads, cfg.head_dim
-    _launch("dg_prefix_attn", q.device, stream, ctypes.byref(cfg), n_seqs,
-            n_tokens, _index(seq_off, "seq_off", n_seqs + 1), _index(kv_len, "kv_len", n_seqs),
-            shared_len, _rows(q, "q", act, n_tokens, hq, hd), _pages(cfg, kv, n_seqs),
-            1 if causal else 0, _rows(out, "out", act, n_tokens, hq, hd), w, wb, _p(dev_status))
+    _launch("dg_prefix_attn", dev, stream, ctypes.byref(cfg), n_seqs, n_tokens,
+            _index(seq_off, "seq_off", n_seqs + 1, dev), _index(kv_len, "kv_len", n_seqs, dev),
+            shared_len, _rows(q, "q", act, n_tokens, hq, hd), _pages(cfg, kv, n_seqs, dev),
+            1 if causal else 0, _rows(out, "out", act, n_tokens, hq, hd, dev=dev), w, wb,
+            _status(dev_status, dev))
 
 
 def dg_debug_wait_probe(limit_cycles, arrive, dev_status, stream=None):

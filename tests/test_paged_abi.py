@@ -72,6 +72,10 @@ def test_attention_refusals():
     wide = _cfg(n_q_heads=65, n_kv_heads=1)
     assert _call("dg_paged_attn", wide, _attn_args(kv)) == B.DG_ERR_UNSUPPORTED
     assert B.dg_paged_workspace_size(wide, 2, 5) == 0
+    # more steps of work than the split's 32-bit costs hold
+    a = _attn_args(_kv(max_pages=1 << 20, page_size=1024))
+    a[0] = a[1] = 64
+    assert _call("dg_paged_attn", cfg, a) == B.DG_ERR_UNSUPPORTED
     # shared prefix: positive, whole pages, within the page table
     for shared in (0, -64, 32, 320):
         a = _attn_args(kv)
@@ -140,3 +144,52 @@ def test_binding_refuses_misfits():
         B._index(t(4, dtype=torch.int64), "seq_off", 2)
     with pytest.raises(ValueError):
         B._index(t(2, dtype=torch.int32), "seq_off", 3)
+
+
+class _Elsewhere:
+    """What the binding asks of a tensor, on a device of its own."""
+
+    def __init__(self, dev, dtype, *shape):
+        self.dev, self.dtype, self.shape, self.ndim = dev, dtype, shape, len(shape)
+
+    def get_device(self):
+        return self.dev
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return math.prod(self.shape)
+
+    def data_ptr(self):
+        return 256
+
+
+def test_binding_refuses_tensors_of_several_devices():
+    n0, cfg, bf = B.dg_launch_count(), _cfg(), torch.bfloat16
+    hq, hkv, hd = cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim
+    kv = object.__new__(B.PagedKV)
+    kv.act, kv.kv_heads, kv.head_dim, kv.seqs = bf, hkv, hd, 2
+    kv.struct = B.DgPagedKv(**PAGES)
+    kv.ref = ctypes.byref(kv.struct)
+    i32 = torch.int32
+    names = ("off", "lens", "q", "out", "ws", "status", "pages")
+    for far in names:
+        dev = {n: 1 if n == far else 0 for n in names}
+        kv.dev = dev["pages"]
+        args = (_Elsewhere(dev["off"], i32, 3), _Elsewhere(dev["lens"], i32, 2))
+        rest = (_Elsewhere(dev["q"], bf, 5, hq, hd), kv, 1, _Elsewhere(dev["out"], bf, 5, hq, hd),
+                _Elsewhere(dev["ws"], torch.uint8, 1 << 30), _Elsewhere(dev["status"], i32, 1))
+        with pytest.raises(ValueError):
+            B.dg_paged_attn(cfg, 2, 5, *args, *rest)
+        with pytest.raises(ValueError):
+            B.dg_prefix_attn(cfg, 2, 5, *args, 64, *rest)
+    for name in ("cache_len", "gain", "status"):
+        t = {"cache_len": _Elsewhere(1, i32, 4), "gain": _Elsewhere(1, torch.float32, hd),
+             "status": _Elsewhere(1, i32, 1)}[name]
+        with pytest.raises(ValueError):
+            {"cache_len": lambda: B._index(t, "cache_len", 4, 0),
+             "gain": lambda: B._gain(cfg, t, "q_gain", 0), "status": lambda: B._status(t, 0)}[name]()
+    with pytest.raises(ValueError):                       # a status word of another type
+        B._status(_Elsewhere(0, torch.int64, 1), 0)
+    assert B.dg_launch_count() == n0
