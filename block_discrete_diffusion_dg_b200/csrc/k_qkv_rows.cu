@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(Q_THR) qkv_rows_kernel(const __grid_constant__
 // Frequencies theta^(-2j / rot), scaled, in turns per position.  A running product in extended
 // precision: 64 factors keep the relative error near 2^-58.
 void fill_turns(const RopeSpec &r, double *turn) {
-  const long double two_pi = 6.283185307179586476925286766559L;
+  const long double per_turn = 0.159154943091895335768883763372514L;   // 1 / 2 pi
   const long double ratio = r.rot > 0 ? powl((long double)r.theta, -2.0L / r.rot) : 1.0L;
   long double f = 1.0L;
   for (int j = 0; j < r.rot / 2; ++j, f *= ratio) {
@@ -309,12 +309,12 @@ void fill_turns(const RopeSpec &r, double *turn) {
       // "NTK-by-parts" interpolation (Peng et al., 2023, "YaRN"): pairs that turn more than
       // beta_fast times over the original length keep their frequency, those below beta_slow
       // turns are interpolated, a ramp in between
-      const long double turns = r.orig_len * f / two_pi;
+      const long double turns = r.orig_len * f * per_turn;
       long double keep = (turns - r.beta_slow) / (r.beta_fast - r.beta_slow);
       keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
       w = f / r.factor * (1 - keep) + f * keep;
     }
-    turn[j] = (double)(w / two_pi);
+    turn[j] = (double)(w * per_turn);
   }
 }
 

@@ -149,6 +149,8 @@ def test_binding_refuses_misfits():
 class _Elsewhere:
     """What the binding asks of a tensor, on a device of its own."""
 
+    is_cuda = True
+
     def __init__(self, dev, dtype, *shape):
         self.dev, self.dtype, self.shape, self.ndim = dev, dtype, shape, len(shape)
 
@@ -189,7 +191,7 @@ def test_binding_refuses_tensors_of_several_devices():
              "status": _Elsewhere(1, i32, 1)}[name]
         with pytest.raises(ValueError):
             {"cache_len": lambda: B._index(t, "cache_len", 4, 0),
-             "gain": lambda: B._gain(cfg, t, "q_gain", 0), "status": lambda: B._status(t, 0)}[name]()
+             "gain": lambda: B._gain(t, "q_gain", hd, 0), "status": lambda: B._status(t, 0)}[name]()
     with pytest.raises(ValueError):                       # a status word of another type
         B._status(_Elsewhere(0, torch.int64, 1), 0)
     assert B.dg_launch_count() == n0
