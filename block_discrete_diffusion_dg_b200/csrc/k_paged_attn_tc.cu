@@ -152,7 +152,8 @@ __device__ __forceinline__ void p_fail(int32_t *st, volatile int *abort_flag) {
   *abort_flag = 1;
 }
 
-template <int HD>
+// CHAINS false: a call whose items all have few rows; the kernel without what the chains need.
+template <int HD, bool CHAINS>
 __global__ void __launch_bounds__(P_THR, 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(P_THR, 1)
 
   // (the shuffle tells the compiler that a warp's threads agree on it)
   const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  if (warp == 1) {
+  if (CHAINS && warp == 1) {
     if (lane == 0) {
       for (int x = 0; x < 2; ++x) {
         mbar_init(&q_full[x], 1);
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(P_THR, 1)
     __syncwarp();
     tmem_alloc(tmem_slot, P_TMEM);
     tmem_relinquish();
-  } else if (warp == 2 && lane == 0) {
+  } else if (CHAINS && warp == 2 && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -210,14 +211,14 @@ __global__ void __launch_bounds__(P_THR, 1)
   // (the scan's scratch lies where rows will leave the kernel much later)
   const int err = paged_locate<P_THR / 3, 3>(p, blockIdx.x, gridDim.x, PAGED_STARTS, start, io.heads,
                                           *reinterpret_cast<PagedScan *>(sOut));
-  fence_before();
+  if constexpr (CHAINS) fence_before();
   __syncthreads();
-  fence_after();
-  const uint32_t tmem = __shfl_sync(FULL, *tmem_slot, 0);
+  if constexpr (CHAINS) fence_after();
+  const uint32_t tmem = CHAINS ? __shfl_sync(FULL, *tmem_slot, 0) : 0;
   if (threadIdx.x == 0 && blockIdx.x == 0) paged_report(io, err);
   const int rep = io.rep, qn = p.qn;   // qn tokens of rep heads make a query tile
 
-  if (warp == 0) {
+  if (CHAINS && warp == 0) {
     // ---- copies
     reg_dec<P_REGS_LO>();
     const int page = 1 << io.page_shift, box = min(page, KT);
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(P_THR, 1)
     for (uint32_t f = fill > S ? fill - S : 0; f < fill; ++f) (void)mbar_wait(&full[f % S], (f / S) & 1);
     for (int x = 0; x < 2; ++x)
       if (nq[x] > 0) (void)mbar_wait(&q_full[x], (nq[x] - 1) & 1);
-  } else if (warp == 1) {
+  } else if (CHAINS && warp == 1) {
     // ---- matrix products: the warp waits together, one lane issues
     reg_dec<P_REGS_LO>();
     constexpr uint32_t id_s = idesc_bf16(128, KT), id_p = idesc_bf16_bmn(128, HD);
@@ -440,10 +441,10 @@ __global__ void __launch_bounds__(P_THR, 1)
     }
     __syncwarp();
   } else if (warp < 4) {
-    reg_dec<P_REGS_LO>();
+    if constexpr (CHAINS) reg_dec<P_REGS_LO>();
   } else {
     // ---- softmax of chain x
-    reg_inc<P_REGS_HI>();
+    if constexpr (CHAINS) reg_inc<P_REGS_HI>();
     const int x = (warp - 4) >> 2;
     const int q4 = warp & 3;                  // tensor-memory lane quarter of this warp
     const int r = q4 * 32 + lane;             // query row of the tile
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(P_THR, 1)
     const float sl2 = 1.4426950408889634f / sqrtf((float)HD);
     uint32_t ns = 0;                          // key tiles of this chain so far
     bool ok = true;
-    for (int kind = 0; kind < 2 && ok; ++kind) {
+    for (int kind = 0; CHAINS && kind < 2 && ok; ++kind) {
       if (start[kind == PAGED_WIDE ? 0 : 1 + x].u1 == 0) continue;
       PagedWalk w;
       for (w.begin(p, kind, start[kind == PAGED_WIDE ? 0 : 1 + x]); w.more(); w.next(p)) {
@@ -609,14 +610,14 @@ __global__ void __launch_bounds__(P_THR, 1)
     // ---- few-row items
     // this warp has left its chain; when all eight have, the rings and query tiles are idle
     __syncwarp();
-    if (lane == 0) mbar_arrive(chains_done);
+    if (CHAINS && lane == 0) mbar_arrive(chains_done);
     const PagedStart &few_start = start[3 + warp - 4];
     if (ok && few_start.u0 < few_start.u1) {
       constexpr int ROW = HD * 2, SLOT = F_KT * ROW;            // a slot: 32 keys, chunks swizzled
       const int fw = warp - 4, gr = lane >> 2, tq = lane & 3;   // fragment row and column pair
       uint8_t *ring = sQ + fw * F_SLOTS * SLOT;
       const int shift = io.page_shift;
-      ok = __all_sync(FULL, mbar_wait(chains_done, 0));
+      if constexpr (CHAINS) ok = __all_sync(FULL, mbar_wait(chains_done, 0));
       // Copies run F_SLOTS slots ahead of the arithmetic, across items: slot n of the walk is K (n
       // even) or V of a step, one group of cp.async each.  Rows behind the last key are filled
       // with zeros. Each lane holds the first row (for kv head 0) of a page, 32 pages of a
@@ -826,25 +827,40 @@ __global__ void __launch_bounds__(P_THR, 1)
       if (!ok && lane == 0) p_fail(io.status, abort_flag);
     }
   }
-  fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    fence_after();
-    tmem_dealloc(tmem, P_TMEM);
+  if constexpr (CHAINS) {
+    fence_before();
+    __syncthreads();
+    if (warp == 1) {
+      fence_after();
+      tmem_dealloc(tmem, P_TMEM);
+    }
   }
+}
+
+template <int HD, bool CHAINS>
+int launch_tc(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PagedShape &p,
+              const PagedIO &io, cudaStream_t s) {
+  constexpr size_t smem = Tc<HD>::SMEM;
+  note_launch(s, "paged_attn_tc");
+  cudaFuncSetAttribute(paged_attn_tc_kernel<HD, CHAINS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)smem);
+  launch_pdl(paged_attn_tc_kernel<HD, CHAINS>, io.ctas, P_THR, smem, s, tq, tk, tv, p, io);
+  return check_launch("paged_attn_tc");
 }
 
 template <int HD>
 int run_tc(const PagedCall &c, const PagedShape &p, const PagedIO &io, cudaStream_t s) {
-  using C = Tc<HD>;
   // the register split inside the kernel needs the launch to hold P_REGS registers per thread; a
   // build with fewer would leave setmaxnreg.inc waiting, so it is refused here
   static const int regs = [] {
     cudaFuncAttributes fa{};
-    return cudaFuncGetAttributes(&fa, paged_attn_tc_kernel<HD>) == cudaSuccess ? fa.numRegs : -1;
+    return cudaFuncGetAttributes(&fa, paged_attn_tc_kernel<HD, true>) == cudaSuccess ? fa.numRegs : -1;
   }();
   if (regs < P_REGS) return DG_ERR_UNSUPPORTED;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq{}, tk{}, tv{};
+  // So few packed rows that no item can have more than a few (single tokens of a small batch; the
+  // shared prefix, an item over all rows, is one of them too).
+  if (p.n_tokens <= p.qf) return launch_tc<HD, false>(tq, tk, tv, p, io, s);
   const uint64_t rows = (uint64_t)c.n_pages * c.Hkv * c.page_size;
   const uint32_t box = c.page_size < PAGED_TC_KT ? c.page_size : PAGED_TC_KT;
   const CUtensorMapDataType bt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -853,11 +869,7 @@ int run_tc(const PagedCall &c, const PagedShape &p, const PagedIO &io, cudaStrea
   if (rc == DG_OK) rc = make_tmap_2d(&tk, bt, 2, c.k_pages, HD, rows, HD * 2, 64, box);
   if (rc == DG_OK) rc = make_tmap_2d(&tv, bt, 2, c.v_pages, HD, rows, HD * 2, 64, box);
   if (rc != DG_OK) return rc;
-  note_launch(s, "paged_attn_tc");
-  cudaFuncSetAttribute(paged_attn_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)C::SMEM);
-  launch_pdl(paged_attn_tc_kernel<HD>, io.ctas, P_THR, C::SMEM, s, tq, tk, tv, p, io);
-  return check_launch("paged_attn_tc");
+  return launch_tc<HD, true>(tq, tk, tv, p, io, s);
 }
 
 }  // namespace
