@@ -423,7 +423,7 @@ def _misfit(t, name, want, dev):
     raise ValueError(f"{name}: {want} wanted, {t.dtype} {tuple(t.shape)} given")
 
 
-def _rows(t, name, dtype, *shape, dev=None):
+def _rows(t, name, dtype, shape, dev=None):
     """Pointer of a contiguous tensor of this type on device `dev` (None: on any) that holds exactly
     `shape`."""
     if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or
@@ -451,13 +451,14 @@ def _qkv_rows(cfg, qkv, rows, heads=None):
     width, dev = (hq + 2 * hkv) * hd, qkv.get_device()
     if qkv.dtype is not act or qkv.shape != (rows, width):
         raise ValueError(f"qkv: {act} {(rows, width)} wanted, {qkv.dtype} {tuple(qkv.shape)} given")
-    if dev < 0 or qkv.stride(1) != 1:
+    ld, step = qkv.stride()
+    if dev < 0 or step != 1:
         raise ValueError("qkv: device rows of contiguous elements wanted")
-    return qkv.data_ptr(), (qkv.stride(0) if rows > 1 else width), dev
+    return qkv.data_ptr(), (ld if rows > 1 else width), dev
 
 
 def _gain(g, name, hd, dev):
-    return None if g is None else _rows(g, name, torch.float32, hd, dev=dev)
+    return None if g is None else _rows(g, name, torch.float32, (hd,), dev)
 
 
 def _pages(kv: PagedKV, heads, n_seqs, dev):
@@ -509,9 +510,9 @@ def dg_qk_norm_rope(cfg, batch, n_tokens, qkv, cache_len, q_gain, k_gain, rope: 
     _launch("dg_qk_norm_rope", dev, stream, ctypes.byref(cfg), batch, n_tokens, ptr, ld,
             _index(cache_len, "cache_len", batch, dev), _gain(q_gain, "q_gain", hd, dev),
             _gain(k_gain, "k_gain", hd, dev), None if rope is None else ctypes.byref(rope),
-            _rows(q, "q", act, batch, n_tokens, hq, hd, dev=dev),
-            _rows(k_new, "k_new", act, batch, hkv, n_tokens, hd, dev=dev),
-            _rows(v_new, "v_new", act, batch, hkv, n_tokens, hd, dev=dev), _status(dev_status, dev))
+            _rows(q, "q", act, (batch, n_tokens, hq, hd), dev),
+            _rows(k_new, "k_new", act, (batch, hkv, n_tokens, hd), dev),
+            _rows(v_new, "v_new", act, (batch, hkv, n_tokens, hd), dev), _status(dev_status, dev))
 
 
 def dg_paged_append(cfg, n_seqs, n_tokens, seq_off, kv_len, qkv, q_gain, k_gain,
@@ -523,7 +524,7 @@ def dg_paged_append(cfg, n_seqs, n_tokens, seq_off, kv_len, qkv, q_gain, k_gain,
             _index(seq_off, "seq_off", n_seqs + 1, dev), _index(kv_len, "kv_len", n_seqs, dev), ptr,
             ld, _gain(q_gain, "q_gain", hd, dev), _gain(k_gain, "k_gain", hd, dev),
             None if rope is None else ctypes.byref(rope), _pages(kv, heads, n_seqs, dev),
-            None if q is None else _rows(q, "q", act, n_tokens, hq, hd, dev=dev),
+            None if q is None else _rows(q, "q", act, (n_tokens, hq, hd), dev),
             _status(dev_status, dev))
 
 
@@ -546,8 +547,8 @@ def dg_paged_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, q, kv: PagedKV, causal
     heads = act, hq, _, hd = _heads(cfg)
     _launch("dg_paged_attn", dev, stream, ctypes.byref(cfg), n_seqs, n_tokens,
             _index(seq_off, "seq_off", n_seqs + 1, dev), _index(kv_len, "kv_len", n_seqs, dev),
-            _rows(q, "q", act, n_tokens, hq, hd), _pages(kv, heads, n_seqs, dev), 1 if causal else 0,
-            _rows(out, "out", act, n_tokens, hq, hd, dev=dev), w, wb, _status(dev_status, dev))
+            _rows(q, "q", act, (n_tokens, hq, hd)), _pages(kv, heads, n_seqs, dev), 1 if causal else 0,
+            _rows(out, "out", act, (n_tokens, hq, hd), dev), w, wb, _status(dev_status, dev))
 
 
 def dg_prefix_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, shared_len, q, kv: PagedKV, causal, out,
@@ -558,8 +559,8 @@ def dg_prefix_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, shared_len, q, kv: Pa
     heads = act, hq, _, hd = _heads(cfg)
     _launch("dg_prefix_attn", dev, stream, ctypes.byref(cfg), n_seqs, n_tokens,
             _index(seq_off, "seq_off", n_seqs + 1, dev), _index(kv_len, "kv_len", n_seqs, dev),
-            shared_len, _rows(q, "q", act, n_tokens, hq, hd), _pages(kv, heads, n_seqs, dev),
-            1 if causal else 0, _rows(out, "out", act, n_tokens, hq, hd, dev=dev), w, wb,
+            shared_len, _rows(q, "q", act, (n_tokens, hq, hd)), _pages(kv, heads, n_seqs, dev),
+            1 if causal else 0, _rows(out, "out", act, (n_tokens, hq, hd), dev), w, wb,
             _status(dev_status, dev))
 
 

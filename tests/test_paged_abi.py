@@ -139,7 +139,7 @@ def test_binding_refuses_misfits():
     with pytest.raises(ValueError):                       # wrong width
         B._qkv_rows(cfg, t(5, 4000, dtype=torch.bfloat16), 5)
     with pytest.raises(ValueError):
-        B._rows(t(4, 4), "q", torch.bfloat16, 4, 4)
+        B._rows(t(4, 4), "q", torch.bfloat16, (4, 4))
     with pytest.raises(ValueError):
         B._index(t(4, dtype=torch.int64), "seq_off", 2)
     with pytest.raises(ValueError):
