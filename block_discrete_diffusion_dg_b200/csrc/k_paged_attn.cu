@@ -347,8 +347,21 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const int tl = paged_token(io, r);
     return (T *)io.out + ((size_t)(h.tok0 + tl) * io.Hq + h.head * io.rep + r - tl * io.rep) * HD;
   };
+  // few-row items: lane i holds the head of the block's worker i (one after the other, these loads
+  // were a good part of a short call's join)
+  PagedHead mine{};
+  if (few && lane < 8) mine = io.heads[c0 + lane];
+  auto head_of = [&](int w) {
+    PagedHead h{};
+    h.first = __shfl_sync(0xffffffffu, mine.first, w);
+    h.last = __shfl_sync(0xffffffffu, mine.last, w);
+    h.tok0 = __shfl_sync(0xffffffffu, mine.tok0, w);
+    h.tokens = __shfl_sync(0xffffffffu, mine.tokens, w);
+    h.head = __shfl_sync(0xffffffffu, mine.head, w);
+    return h;
+  };
   {
-    const PagedHead h = io.heads[c];
+    const PagedHead h = few ? head_of(warp) : io.heads[c];
     const int rows = h.first >= 0 ? h.tokens * io.rep : 0, n = h.last - h.first + 1;
     const int begin = base + h.first;
     // this warp's rows r0, r0 + step, ... of the item's shares
@@ -385,12 +398,13 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   }
   if (!few) return;
   // few-row items of many pieces: this block's part of their rows
+  // (once per block and item: with the first of the block's workers that goes on with it)
+  unsigned todo = __ballot_sync(0xffffffffu, lane < 8 && mine.first >= 0 && mine.last - mine.first >= MANY &&
+                                                 (lane == 0 || base + mine.first >= c0 + lane - 1));
 #pragma unroll 1
-  for (int w = 0; w < 8; ++w) {
-    const PagedHead h = io.heads[c0 + w];
+  for (; todo; todo &= todo - 1) {
+    const PagedHead h = head_of(__ffs(todo) - 1);
     const int n = h.last - h.first + 1, begin = base + h.first;
-    // once per block and item: with the first of the block's workers that goes on with it
-    if (h.first < 0 || n <= MANY || (w > 0 && begin < c0 + w - 1)) continue;
     // blocks that hold such workers
     const int b0 = (begin + 1 - 3 * io.ctas) / 8, b1 = (begin + n - 1 - 3 * io.ctas) / 8;
     const int rows = h.tokens * io.rep, per = (n + 7) / 8;
@@ -413,13 +427,18 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 }
 
 // Joins each row's result over the shared prefix with the one over its own keys; either may have
-// been cut into pieces.  A warp takes two query heads of a packed row.
-template <typename T, int HD>
-__global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_constant__ PagedShape p,
+// been cut into pieces.  A warp takes NR query heads of a packed row.  A small call's time is the
+// length of the chain of loads that depend on one another, so its warps take one head each (128
+// single tokens over 8192 shared keys, the whole call: 50 us with two heads a warp, 40 with one;
+// 1024 tokens: 177 and 181).  The pieces of a row are folded together, up to 32 at once.
+template <typename T, int HD, int NR>
+__global__ void __launch_bounds__(256, NR == 1 ? 3 : 4) paged_join_prefix_kernel(const __grid_constant__ PagedShape p,
                                                                 const __grid_constant__ PagedIO io) {
   pdl_wait();
   pdl_trigger();
-  constexpr int NR = 2, NS = 4;
+  constexpr int NS = 4;
+  constexpr unsigned full = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
   const int groups = (io.Hq + NR - 1) / NR;
   const long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int tok = (int)(task / groups), h0 = (int)(task % groups) * NR;
@@ -432,15 +451,19 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_con
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       ml[i][k] = io.part_ml[paged_region_row(p, io, k, tok, min(h0 + i, io.Hq - 1))];
-  // the sequence that holds this row, if it is one the attention took
+  // the sequence that holds this row, if it is one the attention took: 32-way search
   int lo = 0, hi = p.n_seqs;
+#pragma unroll 1
   while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (p.seq_off[mid] <= tok) lo = mid;
-    else hi = mid;
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const bool le = i < hi && (i == lo || p.seq_off[i] <= tok);
+    const int l = 31 - __clz(__ballot_sync(full, le));
+    lo += l * step;
+    hi = min(hi, lo + step);
   }
   const PagedSeg s = paged_seg(p, lo + 1);
   if (refused || s.n == 0 || tok < s.tok0 || tok >= s.tok0 + s.n) return;
+  // the pieces of each row: over the prefix (k = 0) and over its own keys
   size_t row[NR][NS];
   bool on[NR][NS], many = false;
   T *dst[NR];
@@ -455,8 +478,8 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_con
       if (ml[i][k].y < 0.f) {  // cut into pieces from this worker on
         const int c = __float_as_int(ml[i][k].x);
         const PagedHead hd = io.heads[c + 1];
-        many = many || hd.last > hd.first + 1;
         const int r = (tok - hd.tok0) * io.rep + hr;
+        many = many || hd.last > hd.first + 1;
         row[i][2 * k] = paged_slot_row(io, c, true, r);
         row[i][2 * k + 1] = paged_slot_row(io, c + 1, false, r);
       }
@@ -469,20 +492,32 @@ __global__ void __launch_bounds__(256) paged_join_prefix_kernel(const __grid_con
   }
 #pragma unroll 1
   for (int h = h0; h < min(h0 + NR, io.Hq); ++h) {
-    const int hr = h % io.rep;
+    // (the region's entries and the heads again: they are in L1 now, and registers hold fewer warps)
+    int first[2], n[2];
+    size_t at[2], next[2];   // rows of the first and the second piece
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      at[k] = next[k] = paged_region_row(p, io, k, tok, h);
+      first[k] = 0;
+      n[k] = 1;
+      const float2 e = io.part_ml[at[k]];
+      if (e.y < 0.f) {
+        first[k] = __float_as_int(e.x);
+        const PagedHead hd = io.heads[first[k] + 1];
+        const int r = (tok - hd.tok0) * io.rep + h % io.rep;
+        n[k] = hd.last - hd.first + 1;
+        at[k] = paged_slot_row(io, first[k], true, r);
+        next[k] = paged_slot_row(io, first[k] + 1, false, r);
+      }
+    }
     Fold<HD> f;
 #pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-      const size_t r = paged_region_row(p, io, which, tok, h);
-      const float2 e = io.part_ml[r];
-      if (e.y < 0.f) {
-        const int c = __float_as_int(e.x);
-        const PagedHead hd = io.heads[c + 1];
-        f.add_range(io, c, c, hd.last + paged_first_worker(io, paged_worker_kind(io, c)),
-                    (tok - hd.tok0) * io.rep + hr);
-      } else {
-        f.add(io.part_o, 1, e, r);
-      }
+    for (int j0 = 0; j0 < n[0] + n[1]; j0 += 32) {   // the prefix's pieces, then its own
+      const int j = min(j0 + lane, n[0] + n[1] - 1), k = j < n[0] ? 0 : 1, i = k ? j - n[0] : j;
+      const int kind = paged_worker_kind(io, k ? first[1] : first[0]);
+      const size_t later = (k ? next[1] : next[0]) + (size_t)2 * (i - 1) * io.rows[kind];
+      const size_t r = i > 0 ? later : k ? at[1] : at[0];
+      f.add(io.part_o, min(32, n[0] + n[1] - j0), io.part_ml[r], r);
     }
     f.store((T *)io.out + ((size_t)tok * io.Hq + h) * HD);
   }
@@ -501,8 +536,14 @@ template <typename T, int HD>
 int run_join(const PagedShape &p, const PagedIO &io, cudaStream_t s) {
   if (p.shared_len > 0) {
     note_launch(s, "paged_join_prefix");
-    const long long tasks = (long long)p.n_tokens * ((io.Hq + 1) / 2);
-    launch_pdl(paged_join_prefix_kernel<T, HD>, (unsigned)((tasks + 7) / 8), 256, 0, s, p, io);
+    // rows that the device holds at once (8 blocks of 8 warps an SM): a head each, else two
+    if ((long long)p.n_tokens * io.Hq <= 64LL * num_sms()) {
+      const long long tasks = (long long)p.n_tokens * io.Hq;
+      launch_pdl(paged_join_prefix_kernel<T, HD, 1>, (unsigned)((tasks + 7) / 8), 256, 0, s, p, io);
+    } else {
+      const long long tasks = (long long)p.n_tokens * ((io.Hq + 1) / 2);
+      launch_pdl(paged_join_prefix_kernel<T, HD, 2>, (unsigned)((tasks + 7) / 8), 256, 0, s, p, io);
+    }
     return check_launch("paged_join_prefix");
   }
   // no item of a kind can exist with fewer rows than it takes
