@@ -236,6 +236,17 @@ struct Fold {
   __device__ __forceinline__ void add(const float *__restrict__ part_o, int n, float2 ml,
                                       size_t row) {
     const int lane = threadIdx.x & 31;
+    constexpr int U = 8;   // rows in flight
+    float x[U][V];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const size_t r = __shfl_sync(0xffffffffu, row, min(i0 + i, n - 1));
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[i][v] = i0 + i < n ? part_o[r * HD + lane * V + v] : 0.f;
+      }
+    };
+    load(0);   // (before the statistics are asked for: one latency, not two)
     const float mn = fmaxf(m, warp_max(lane < n ? ml.x : -INFINITY));
     const float base = mn == -INFINITY ? 0.f : mn;
     const float f = exp2f(m - base);
@@ -244,15 +255,8 @@ struct Fold {
     l = l * f + warp_sum(lane < n ? c * ml.y : 0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= f;
-    constexpr int U = 8;   // rows in flight
     for (int i0 = 0; i0 < n; i0 += U) {
-      float x[U][V];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const size_t r = __shfl_sync(0xffffffffu, row, min(i0 + i, n - 1));
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[i][v] = i0 + i < n ? part_o[r * HD + lane * V + v] : 0.f;
-      }
+      if (i0 > 0) load(i0);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const float ci = __shfl_sync(0xffffffffu, c, (i0 + i) & 31);
