@@ -364,6 +364,28 @@ def test_extreme_scores(act, hq, hkv, hd, n):
         check_attention(out, q, c, new, have, causal, act)
 
 
+@pytest.mark.parametrize("act,hq,hkv,hd", [("bf16", 16, 8, 128), ("bf16", 4, 4, 64), ("bf16", 16, 1, 128),
+                                           ("bf16", 32, 1, 64), ("f32", 4, 2, 64)])
+@pytest.mark.parametrize("shared", [0, 64, 8192])
+def test_batches_of_a_few_rows(act, hq, hkv, hd, shared):
+    """Calls whose rows all fit few-row items, and the first that do not: one row and several, short
+    contexts and ones cut into more pieces than a warp has lanes, with rows of nobody's behind."""
+    g, most = gen(19), max(16 * hkv // hq, 1)
+    cfg = make_cfg(act, hq, hkv, hd)
+    for new, own in (([1], [0]), ([1], [9000]), ([most], [300]), ([most + 1], [300]),
+                     ([1] * (most // 2) + [0, most - most // 2], [700] * (most // 2) + [5, 40])):
+        have = [shared + o for o in own]
+        c = Cache(g, act, hkv, hd, 64, [n + h for n, h in zip(new, have)], shared=shared)
+        rows = sum(new)
+        for padded in {rows, max(rows, most)}:
+            q = randn(g, padded, hq, hd).to(DT[act])
+            for causal in (0, 1):
+                out, st = run_attention(cfg, c, new, have, q, causal, shared=shared)
+                assert st == B.DG_OK
+                check_attention(out[:rows], q[:rows], c, new, have, causal, act)
+                assert (out[rows:].float() == MARK).all()
+
+
 @pytest.mark.parametrize("act,hq,hkv,hd", [("bf16", 16, 8, 128), ("f32", 4, 2, 64)])
 @pytest.mark.parametrize("shared", [0, 1024])
 def test_largest_page(act, hq, hkv, hd, shared):
