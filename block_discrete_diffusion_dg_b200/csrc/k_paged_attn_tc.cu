@@ -152,7 +152,7 @@ __device__ __forceinline__ void p_fail(int32_t *st, volatile int *abort_flag) {
   *abort_flag = 1;
 }
 
-// CHAINS false: a call whose items all have few rows; the kernel without what the chains need.
+// CHAINS false: a call whose items all are few-row; the kernel without what the chains need.
 template <int HD, bool CHAINS>
 __global__ void __launch_bounds__(P_THR, 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -858,9 +858,7 @@ int run_tc(const PagedCall &c, const PagedShape &p, const PagedIO &io, cudaStrea
   }();
   if (regs < P_REGS) return DG_ERR_UNSUPPORTED;
   CUtensorMap tq{}, tk{}, tv{};
-  // So few packed rows that no item can have more than a few (single tokens of a small batch; the
-  // shared prefix, an item over all rows, is one of them too).
-  if (p.n_tokens <= p.qf) return launch_tc<HD, false>(tq, tk, tv, p, io, s);
+  if (paged_all_few(p)) return launch_tc<HD, false>(tq, tk, tv, p, io, s);
   const uint64_t rows = (uint64_t)c.n_pages * c.Hkv * c.page_size;
   const uint32_t box = c.page_size < PAGED_TC_KT ? c.page_size : PAGED_TC_KT;
   const CUtensorMapDataType bt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

@@ -35,7 +35,7 @@ struct PagedShape {
   int Hkv;
   int qt;                   // tokens per item
   int qn;                   // a last item of at most qn tokens is narrow (0: none is),
-  int qf;                   // of at most qf <= qn few-row (0: none is)
+  int qf;                   // of at most qf <= qn few-row (0: none is; qf == qt: every item is)
   // by kind of item:
   int kt_shift[3];          // keys per tile: 2^kt_shift
   int start_cost[3];        // cost of starting and storing an item, in key tiles
@@ -130,20 +130,23 @@ enum { PAGED_WIDE = 0, PAGED_NARROW = 1, PAGED_FEW = 2 };
 
 // Full items of a segment (a division is skipped where there are none: single tokens).
 DG_HD int paged_full_items(const PagedShape &p, const PagedSeg &s) { return s.n < p.qt ? 0 : s.n / p.qt; }
-// The kind of a segment's last item where it is not wide, else PAGED_WIDE.
+DG_HD bool paged_all_few(const PagedShape &p) { return p.qf == p.qt; }
+// The kind of a segment's last item where it is not wide, else PAGED_WIDE (not asked where every item
+// is few-row).
 DG_HD int paged_tail_kind(const PagedShape &p, const PagedSeg &s) {
   const int tail = s.n - paged_full_items(p, s) * p.qt;
   return tail == 0 || tail > p.qn ? PAGED_WIDE : tail > p.qf ? PAGED_NARROW : PAGED_FEW;
 }
 // Items of a kind in one kv head of segment s, and the index of the first.
 DG_HD int paged_items(const PagedShape &p, const PagedSeg &s, int kind) {
+  if (paged_all_few(p)) return kind != PAGED_FEW ? 0 : s.n <= p.qt ? 1 : (s.n + p.qt - 1) / p.qt;
   const int tail = paged_tail_kind(p, s);
   if (kind != PAGED_WIDE) return tail == kind ? 1 : 0;
   const int full = paged_full_items(p, s);
   return full + (tail == PAGED_WIDE && full * p.qt < s.n ? 1 : 0);
 }
 DG_HD int paged_first_item(const PagedShape &p, const PagedSeg &s, int kind) {
-  return kind == PAGED_WIDE ? 0 : paged_full_items(p, s);
+  return kind == PAGED_WIDE || paged_all_few(p) ? 0 : paged_full_items(p, s);
 }
 DG_HD int paged_item_tokens(const PagedShape &p, const PagedSeg &s, int i) {
   const int left = s.n - i * p.qt;
@@ -163,8 +166,9 @@ DG_HD int paged_item_tiles(const PagedShape &p, const PagedSeg &s, int kind, int
 // Cost of the first q items of a kind (of one kv head).
 DG_HD int paged_cost_before(const PagedShape &p, const PagedSeg &s, int kind, int q) {
   if (q <= 0) return 0;
-  // a kind other than wide has one item, which sees all of the segment's keys
-  if (kind != PAGED_WIDE || !s.causal) return q * (paged_tiles(p, kind, s.keys) + p.start_cost[kind]);
+  // a kind other than wide has one item, which sees all of the segment's keys; so has a last one
+  if (!s.causal || (q == 1 && s.n <= p.qt) || (kind != PAGED_WIDE && !paged_all_few(p)))
+    return q * (paged_tiles(p, kind, s.keys) + p.start_cost[kind]);
   const int last = q * p.qt > s.n ? 1 : 0;   // an item with fewer tokens: by itself
   const int kt = 1 << p.kt_shift[kind];
   const int full = floor_sum(q - last, kt, p.qt, s.keys - s.n + p.qt + kt - 1);
@@ -179,7 +183,8 @@ inline long long paged_cost_bound(const PagedShape &p) {
   for (int kind = 0; kind < 3; ++kind) {
     const long long tiles = (p.cap >> p.kt_shift[kind]) + 1 + p.start_cost[kind];
     const long long tails = (p.n_seqs < p.n_tokens ? p.n_seqs : p.n_tokens) + 1;
-    const long long items = kind == PAGED_WIDE ? 2 * (long long)(p.n_tokens / p.qt) + tails : tails;
+    const bool many = kind == PAGED_WIDE || (kind == PAGED_FEW && paged_all_few(p));
+    const long long items = many ? 2 * (long long)(p.n_tokens / p.qt) + tails : tails;
     const long long c = p.Hkv * items * tiles;
     most = c > most ? c : most;
   }
@@ -337,7 +342,7 @@ __device__ __forceinline__ int paged_locate(const PagedShape &p, int cta, int ct
       r.head = (r.u0 - r.item_u0) / each;
       r.item_u0 += r.head * each;
       // the last item that begins at or before u0: 32-way search
-      if (kind == PAGED_WIDE) {
+      if (kind == PAGED_WIDE || (paged_all_few(p) && r.s.n > p.qt)) {
         int a = 0, b = paged_items(p, r.s, kind);
 #pragma unroll 1
         while (b - a > 1) {
@@ -421,10 +426,11 @@ struct PagedWalk {
   }
 };
 
-// The walk of few-row items alone: a segment has at most one, the same for every kv head, so that
-// going on costs a few operations and, at the end of a sequence's heads, the lengths of the next.
+// The walk of few-row items alone: a segment mostly has one at most, the same for every kv head, so
+// that going on costs a few operations and, at the end of a sequence's heads, the lengths of the next.
 struct PagedFewWalk {
   int seq, head, seg, which;          // which: 0 the shared prefix, 1 the sequence's own keys
+  int index, items;                   // the current of the segment's items
   int tok, toks;                      // packed rows [tok, tok + toks)
   int key0, keys, tiles;              // keys [key0, key0 + keys)
   int before;                         // keys that the first of the rows sees besides itself; < 0: all
@@ -433,14 +439,15 @@ struct PagedFewWalk {
   DG_HD bool more() const { return t0 < t1; }
   DG_HD bool whole() const { return t0 == 0 && t1 == tiles; }
   DG_HD void take(const PagedShape &p, const PagedSeg &s) {
-    const int first = paged_full_items(p, s) * p.qt;
+    const int item = paged_first_item(p, s, PAGED_FEW) + index, first = item * p.qt;
+    items = paged_items(p, s, PAGED_FEW);
     seq = s.seq;
     tok = s.tok0 + first;
-    toks = s.n - first;
+    toks = paged_item_tokens(p, s, item);
     key0 = s.key0;
-    keys = s.keys;
-    tiles = paged_tiles(p, PAGED_FEW, s.keys);
-    before = s.causal ? s.keys - toks : -1;
+    keys = paged_item_keys(p, s, item);
+    tiles = paged_tiles(p, PAGED_FEW, keys);
+    before = s.causal ? keys - toks : -1;
     which = p.shared_len > 0 && seg == 0 ? 0 : 1;
   }
   DG_HD void range(const PagedShape &p, int done) {   // `done`: cost of the item before the range
@@ -451,13 +458,20 @@ struct PagedFewWalk {
   DG_HD void next(const PagedShape &p) {
     t0 = t1 = 0;
     if (left <= 0) return;
-    if (++head == p.Hkv) {
+    const bool many = items > 1;
+    if (++index == items) {
+      index = 0;
+      ++head;
+    }
+    if (head == p.Hkv) {
       head = 0;
       PagedSeg s;
       do {  // cost remains, so a later segment has an item
         s = paged_seg(p, ++seg);
-      } while (s.n == 0 || paged_tail_kind(p, s) != PAGED_FEW);
+      } while (s.n == 0 || paged_items(p, s, PAGED_FEW) == 0);
       take(p, s);
+    } else if (many) {
+      take(p, paged_seg(p, seg));
     }
     range(p, 0);
     left -= tiles + p.start_cost[PAGED_FEW];
@@ -468,6 +482,7 @@ struct PagedFewWalk {
     if (left <= 0) return;
     seg = st.seg;
     head = st.head;
+    index = st.item;
     take(p, st.s);
     range(p, st.u0 - st.item_u0);
     left -= tiles + p.start_cost[PAGED_FEW] - (st.u0 - st.item_u0);

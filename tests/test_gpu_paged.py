@@ -386,6 +386,23 @@ def test_batches_of_a_few_rows(act, hq, hkv, hd, shared):
                 assert (out[rows:].float() == MARK).all()
 
 
+@pytest.mark.parametrize("hq,hkv,hd", [(16, 8, 128), (3, 3, 64), (16, 1, 128), (5, 1, 64)])
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("kind", ["tokens", "pairs", "one_prompt", "prompts"])
+def test_as_many_sequences_as_rows(hq, hkv, hd, causal, kind):
+    """Batches that look like single tokens by their sizes, and are, or are prompts among empty
+    sequences."""
+    g, rng = gen(20), random.Random(hq * 10 + causal)
+    new = {"tokens": [1] * 90, "pairs": [2, 0, 1, 1, 0, 2] * 15, "one_prompt": [0] * 40 + [150] + [0] * 120,
+           "prompts": [33, 0, 70, 1, 0, 47] + [0] * 150}[kind]
+    have = [rng.choice((0, 1, 31, 32, 33, 300, 2500)) for _ in new]
+    c = Cache(g, "bf16", hkv, hd, 32, [n + h for n, h in zip(new, have)])
+    q = randn(g, sum(new), hq, hd).to(torch.bfloat16)
+    out, st = run_attention(make_cfg("bf16", hq, hkv, hd), c, new, have, q, causal)
+    assert st == B.DG_OK
+    check_attention(out, q, c, new, have, causal, "bf16")
+
+
 @pytest.mark.parametrize("act,hq,hkv,hd", [("bf16", 16, 8, 128), ("f32", 4, 2, 64)])
 @pytest.mark.parametrize("shared", [0, 1024])
 def test_largest_page(act, hq, hkv, hd, shared):

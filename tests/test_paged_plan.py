@@ -61,6 +61,9 @@ int main() {
     p.qt = (wide ? 128 : 64) / rep * (wide ? 2 : 1);
     p.qn = wide ? 128 / rep : 0;
     p.qf = wide && rnd(2) ? 16 / rep : 0;
+    const bool few = p.qf > 0 && rnd(2);   // every item few-row
+    if (few) p.qt = p.qn = p.qf;
+    CHECK(paged_all_few(p) == few);
     p.causal = rnd(2);
     p.shared_len = rnd(3) ? 0 : page * (1 + rnd(20));
     p.cap = p.shared_len + 100000;
@@ -84,7 +87,15 @@ int main() {
         CHECK(s.error == 0);
         if (s.n == 0) { CHECK(paged_head_cost(p, s, kind) == 0); continue; }
         const int first = paged_first_item(p, s, kind), n = paged_items(p, s, kind);
-        if (kind == 0) {   // every token in one item of one kind
+        if (few) {         // every token in one few-row item
+          CHECK(kind == 2 || n == 0);
+          int rows = 0;
+          for (int q = 0; q < n; ++q) {
+            CHECK(paged_item_tokens(p, s, q) > 0 && paged_item_tokens(p, s, q) <= p.qf);
+            rows += paged_item_tokens(p, s, q);
+          }
+          CHECK(first == 0 && rows == (kind == 2 ? s.n : 0));
+        } else if (kind == 0) {   // every token in one item of one kind
           int rows = 0;
           for (int q = 0; q < n; ++q) rows += paged_item_tokens(p, s, q);
           const int tail = paged_tail_kind(p, s);
