@@ -413,7 +413,7 @@ _ACT = {DG_F32: torch.float32, DG_BF16: torch.bfloat16}
 
 # A call for a few rows takes the device less time than the host, so the checks are one expression
 # each and say what was wrong only on the way out (with a call per property, and the config's fields
-# read by each, dg_qk_norm_rope took 9.7 us of host time; now 8.8).
+# read by each, dg_qk_norm_rope took 9.7 us of host time; now 8.7).
 def _misfit(t, name, want, dev):
     here = t.get_device()
     if here < 0 or not t.is_contiguous():
