@@ -635,8 +635,11 @@ int launch_paged_attn(const PagedCall &c, void *ws, cudaStream_t s) {
   // known here, so the rule is a row per sequence on average; a prompt among empty sequences comes out
   // right, but its keys are read once per 16 rows (512 rows over 4512 keys among 511 empty ones: 169 us
   // where the chains take 46).
-  if (p.qf > 0 && (c.n_tokens <= p.qf || (c.shared_len == 0 && c.n_tokens <= c.n_seqs)))
-    p.qt = p.qn = p.qf;
+  if (p.qf > 0 && (c.n_tokens <= p.qf || (c.shared_len == 0 && c.n_tokens <= c.n_seqs))) {
+    PagedShape few = p;
+    few.qt = few.qn = few.qf;
+    if (paged_cost_bound(few) <= PAGED_COST_LIMIT) p = few;
+  }
   if (paged_cost_bound(p) > PAGED_COST_LIMIT) return DG_ERR_UNSUPPORTED;
   io.q = c.q;
   io.out = c.out;

@@ -471,8 +471,9 @@ size_t dg_paged_workspace_size(const dg_config *cfg, int n_seqs, int n_tokens, i
  *   q, out [n_tokens][Hq][hd].  out may not overlap q.
  * Scores, softmax statistics and sums are fp32; with bf16 activations of head_dim 64 or 128 the
  * softmax's numerators are rounded to bf16 for the tensor cores.  DG_ERR_UNSUPPORTED where Hq / Hkv >
- * 64, or where the sizes given (n_seqs, n_tokens, max_pages) allow more than 2^30 steps of work (far
- * beyond a million packed tokens over a million keys of a few kv heads).
+ * 64, or where the sizes given (n_seqs, n_tokens, max_pages) allow more than 2^30 steps of work; a
+ * step is one kv head's, up to 16 rows against 32 keys or 256 rows against 128 keys (4096 single
+ * tokens, each with room for 131072 keys of 8 kv heads: 2^27).
  * The values of keys a sequence holds must be finite, those of later tokens of its batch included: a
  * non-finite value may reach the rows before it. */
 int dg_paged_attn(const dg_config *cfg, int n_seqs, int n_tokens, const int32_t *seq_off,
