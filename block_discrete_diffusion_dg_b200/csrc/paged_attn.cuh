@@ -59,9 +59,8 @@ __device__ __forceinline__ void paged_report(const PagedIO &io, int error) {
 }
 
 // ---- destinations
-// ------------------------------------------------------------------------------- Workers are
-// numbered through: wide ones [0, ctas), narrow ones (two per CTA) [ctas, 3 ctas), few-row ones
-// (eight per CTA) [3 ctas, 11 ctas).
+// Workers are numbered through: wide ones [0, ctas), narrow ones (two per CTA) [ctas, 3 ctas), few-row
+// ones (eight per CTA) [3 ctas, 11 ctas).
 __host__ __device__ inline int paged_first_worker(const PagedIO &io, int kind) {
   return kind == PAGED_WIDE ? 0 : kind == PAGED_NARROW ? io.ctas : 3 * io.ctas;
 }
