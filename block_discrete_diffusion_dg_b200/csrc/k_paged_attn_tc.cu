@@ -623,12 +623,13 @@ __global__ void __launch_bounds__(P_THR, 1)
       if constexpr (CHAINS) ok = __all_sync(FULL, mbar_wait(chains_done, 0));
       // Copies run F_SLOTS slots ahead of the arithmetic, across items: slot n of the walk is K (n
       // even) or V of a step, one group of cp.async each.  Rows behind the last key are filled
-      // with zeros. Each lane holds the first row (for kv head 0) of a page, 32 pages of a
-      // sequence at a time. The loading side walks the items and leaves each piece's description
-      // for the computing side.
+      // with zeros. Each lane holds the place of a page, 32 pages of a sequence at a time
+      // (PagedWindow). The loading side walks the items and leaves each piece's description for the
+      // computing side.
       PagedFewWalk lw;
       lw.begin(p, few_start);
-      int lt = lw.t0, ids = 0, ids_seg = -1, ids_page = 0;
+      PagedWindow win;
+      int lt = lw.t0, ids = 0;   // ids: first row (for kv head 0) of the window's page `lane`, -1: none
       bool lv = false;
       uint32_t ls_slot = 0, slot = 0;                           // slots loaded and used next
       FewPiece *pieces = reinterpret_cast<FewPiece *>(stage);   // [4], this warp's
@@ -793,11 +794,9 @@ __global__ void __launch_bounds__(P_THR, 1)
           }
           const int pos = lw.key0 + lt * F_KT, pg = pos >> shift, live = lw.keys - lt * F_KT;
           const int pg2 = (pos + 16) >> shift;   // page of the second 16 keys
-          if (lw.seg != ids_seg || pg < ids_page || pg2 >= ids_page + 32) {
-            ids_seg = lw.seg;
-            ids_page = pg;
+          if (win.move(lw, pg, pg2)) {
             ids = -1;
-            if (pg + lane <= (lw.key0 + lw.keys - 1) >> shift) {
+            if (win.filled(lw, lane, shift)) {
               const long long row = paged_row(io, p, lw.seq, 0, (pg + lane) << shift);
               ids = row < 0 ? -1 : (int)row;
             }
@@ -808,7 +807,7 @@ __global__ void __launch_bounds__(P_THR, 1)
           const int c = lane % CPR, r0 = lane / CPR;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const int first = __shfl_sync(FULL, ids, (g ? pg2 : pg) - ids_page);
+            const int first = __shfl_sync(FULL, ids, (g ? pg2 : pg) - win.first);
             const int at = first + (lw.head << shift) + ((pos + 16 * g) & ((1 << shift) - 1));
             const bf16 *src = pool + (size_t)(first < 0 ? 0 : at) * HD + c * 8;
 #pragma unroll

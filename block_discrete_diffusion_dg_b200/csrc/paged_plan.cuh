@@ -434,6 +434,7 @@ struct PagedFewWalk {
   int tok, toks;                      // packed rows [tok, tok + toks)
   int key0, keys, tiles;              // keys [key0, key0 + keys)
   int before;                         // keys that the first of the rows sees besides itself; < 0: all
+  int seg_end;                        // key behind the segment's last
   int t0, t1, left;                   // tiles of this piece; cost left in the range from its item on
 
   DG_HD bool more() const { return t0 < t1; }
@@ -448,6 +449,7 @@ struct PagedFewWalk {
     keys = paged_item_keys(p, s, item);
     tiles = paged_tiles(p, PAGED_FEW, keys);
     before = s.causal ? keys - toks : -1;
+    seg_end = s.key0 + s.keys;
     which = p.shared_len > 0 && seg == 0 ? 0 : 1;
   }
   DG_HD void range(const PagedShape &p, int done) {   // `done`: cost of the item before the range
@@ -487,6 +489,27 @@ struct PagedFewWalk {
     range(p, st.u0 - st.item_u0);
     left -= tiles + p.start_cost[PAGED_FEW] - (st.u0 - st.item_u0);
     if (t0 >= t1) next(p);   // (a range that ends within the first item's starting cost ends here)
+  }
+};
+
+// The pages whose places a warp holds while it copies keys of a few-row walk: PAGED_WINDOW pages of one
+// segment from `first` on, as far as the segment has them.  It stays while the walk is in the segment and
+// within these pages, from one item to the next too, so it is filled up to the segment's last page: a
+// causal segment's next item sees keys that the one which moved the window here did not.
+constexpr int PAGED_WINDOW = 32;
+struct PagedWindow {
+  int seg = -1, first = 0;
+
+  // Moves to page `page` unless pages page .. page2 are in the window; true if it moved.
+  DG_HD bool move(const PagedFewWalk &w, int page, int page2) {
+    if (w.seg == seg && page >= first && page2 < first + PAGED_WINDOW) return false;
+    seg = w.seg;
+    first = page;
+    return true;
+  }
+  // Whether the i-th place holds a page of the segment.
+  DG_HD bool filled(const PagedFewWalk &w, int i, int page_shift) const {
+    return first + i <= (w.seg_end - 1) >> page_shift;
   }
 };
 

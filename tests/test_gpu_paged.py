@@ -403,6 +403,41 @@ def test_as_many_sequences_as_rows(hq, hkv, hd, causal, kind):
     check_attention(out, q, c, new, have, causal, "bf16")
 
 
+@pytest.mark.parametrize("hq,hkv,hd", [(16, 8, 128), (5, 1, 64), (16, 1, 128)])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("have", [0, 50])
+def test_tokens_prompt_and_idle_slots(hq, hkv, hd, page, have):
+    """A serving batch of 256 slots: 199 single tokens over one long context, a prompt of 40 tokens, the
+    rest idle.  A worker's range holds several of the prompt's items, each of which sees more pages than
+    the one before."""
+    g, keys = gen(21), 8192
+    c = Cache(g, "bf16", hkv, hd, page, [keys, 40 + have])
+    table = torch.full((256, c.table.shape[1]), -1, dtype=torch.int32, device="cuda")
+    table[:199], table[199] = c.table[0], c.table[1]     # (pages may be shared: none is written here)
+    c.kv = B.PagedKV(c.k, c.v, table)
+    new, lens = [1] * 199 + [40] + [0] * 56, [keys - 1] * 199 + [have] + [0] * 56
+    q = (1.5 * randn(g, 239, hq, hd)).to(torch.bfloat16)
+    for causal in (1, 0):
+        out, st = run_attention(make_cfg("bf16", hq, hkv, hd), c, new, lens, q, causal)
+        assert st == B.DG_OK
+        for s, rows, h, mask in ((0, slice(0, 199), keys - 1, 0), (1, slice(199, 239), have, causal)):
+            k, v = c.kept[s]
+            want, A, e = P.attention(q[rows], k, v, mask, h)
+            bound = P.attention_bound(want, A, e, k.shape[0], torch.bfloat16, 2.0 ** -8)
+            assert P.worst(out[rows], want, bound) <= 1.0
+
+
+@pytest.mark.parametrize("hq,hkv,hd,page", [(8, 2, 128, 16), (8, 2, 64, 64), (5, 5, 64, 32)])
+def test_long_prompt_among_idle_slots(hq, hkv, hd, page):
+    g, n = gen(22), 2048
+    new, have = [0] * 700 + [n] + [0] * 1347, [0] * 2048
+    c = Cache(g, "bf16", hkv, hd, page, [a + h for a, h in zip(new, have)])
+    q = (1.5 * randn(g, n, hq, hd)).to(torch.bfloat16)
+    out, st = run_attention(make_cfg("bf16", hq, hkv, hd), c, new, have, q, 1)
+    assert st == B.DG_OK
+    check_attention(out, q, c, new, have, 1, "bf16")
+
+
 @pytest.mark.parametrize("act,hq,hkv,hd", [("bf16", 16, 8, 128), ("f32", 4, 2, 64)])
 @pytest.mark.parametrize("shared", [0, 1024])
 def test_largest_page(act, hq, hkv, hd, shared):

@@ -226,3 +226,107 @@ def test_work_split_covers_every_unit_once(tmp_path):
                     str(exe)], check=True, capture_output=True, text=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+WINDOW = SRC.split("int main()")[0] + r'''
+// Walks every worker's few-row range as the loading side of a warp does: 32 keys a step, their pages from
+// a window that moves with them.  Every 16 keys that a piece has must find their page in it.
+static int walk(const PagedShape &p, int page_shift, int workers) {
+  for (int c = 0; c < workers; ++c) {
+    PagedFewWalk w;
+    PagedWindow win;
+    int held[PAGED_WINDOW] = {};   // page in each place, -1: none
+    for (w.begin(p, locate(p, 2, c, workers)); w.more(); w.next(p)) {
+      const PagedSeg s = paged_seg(p, w.seg);
+      CHECK(w.seg_end == s.key0 + s.keys);
+      for (int t = w.t0; t < w.t1; ++t) {
+        const int pos = w.key0 + t * 32, live = w.keys - t * 32;
+        const int page[2] = {pos >> page_shift, (pos + 16) >> page_shift};
+        if (win.move(w, page[0], page[1])) {
+          for (int i = 0; i < PAGED_WINDOW; ++i) {
+            held[i] = win.filled(w, i, page_shift) ? page[0] + i : -1;
+            // nothing behind the segment's last key is looked up
+            CHECK(held[i] < 0 || held[i] << page_shift < s.key0 + s.keys);
+          }
+        }
+        for (int g = 0; g < 2; ++g) {
+          const int i = page[g] - win.first;
+          CHECK(i >= 0 && i < PAGED_WINDOW);
+          CHECK(16 * g >= live || held[i] == page[g]);
+        }
+      }
+    }
+  }
+  return 0;
+}
+
+// A call that takes every item for few-row.
+static int batch(int rep, int heads, int page_shift, int causal, int shared, int workers,
+                 const std::vector<int> &news, const std::vector<int> &have) {
+  std::vector<int> off(1, 0), kv;
+  for (size_t s = 0; s < news.size(); ++s) {
+    off.push_back(off.back() + news[s]);
+    kv.push_back(shared + have[s]);
+  }
+  PagedShape p{};
+  p.Hkv = heads;
+  p.kt_shift[0] = p.kt_shift[1] = 7;
+  p.kt_shift[2] = 5;
+  p.qt = p.qn = p.qf = 16 / rep;
+  p.start_cost[2] = 1;
+  p.causal = causal;
+  p.shared_len = shared;
+  p.cap = 1 << 20;
+  p.seq_off = off.data();
+  p.kv_len = kv.data();
+  p.n_seqs = (int)news.size();
+  p.n_tokens = off.back() > 0 ? off.back() : 1;
+  return walk(p, page_shift, workers);
+}
+
+int main() {
+  // single tokens over long caches, one short prompt, idle slots
+  for (int page_shift = 4; page_shift <= 10; page_shift += 2)
+    for (int rep = 1; rep <= 16; rep *= 2)
+      for (int have : {0, 10, 50, 500}) {
+        std::vector<int> news(199, 1), kv(199, 8191);
+        news.push_back(40);
+        kv.push_back(have);
+        news.resize(256, 0);
+        kv.resize(256, 0);
+        CHECK(batch(rep, 2, page_shift, 1, 0, 148 * 8, news, kv) == 0);
+      }
+  // one prompt among empty sequences
+  for (int page_shift = 4; page_shift <= 6; ++page_shift) {
+    std::vector<int> news(300, 0), kv(300, 0);
+    news[7] = 2048;
+    CHECK(batch(4, 2, page_shift, 1, 0, 148, news, kv) == 0);
+  }
+  for (int t = 0; t < 600; ++t) {   // random ones, ranges of any length
+    const int seqs = 1 + rnd(40), page_shift = 4 + rnd(7);
+    std::vector<int> news, kv;
+    for (int s = 0; s < seqs; ++s) {
+      news.push_back(rnd(3) ? (rnd(3) ? 1 : rnd(400)) : 0);
+      kv.push_back(rnd(3) ? rnd(3000) : 0);
+    }
+    const int shared = rnd(3) ? 0 : (1 << page_shift) * (1 + rnd(5));
+    CHECK(batch(1 + rnd(16), 1 + rnd(3), page_shift, rnd(4) > 0, shared, rnd(2) ? 1 + rnd(12) : 148, news, kv) == 0);
+  }
+  std::puts("ok");
+  return 0;
+}
+'''
+
+
+def test_page_window_of_few_row_walks(tmp_path):
+    """The places of pages that a few-row warp holds are those of all keys it copies, whatever items of
+    a sequence its range goes on with."""
+    src = tmp_path / "window.cpp"
+    src.write_text(WINDOW)
+    exe = tmp_path / "window"
+    csrc = os.path.join(ROOT, "block_discrete_diffusion_dg_b200", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O2", "-Wall", "-Wextra", "-Werror",
+                    "-fsanitize=undefined", "-fno-sanitize-recover", "-I", csrc, str(src), "-o",
+                    str(exe)], check=True, capture_output=True, text=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
