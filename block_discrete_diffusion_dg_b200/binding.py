@@ -7,6 +7,7 @@ library is missing, :func:`lib` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -214,8 +215,15 @@ def dg_workspace_size(cfg: DgConfig, batch: int, n_tokens: int, cache_cap: int) 
     return lib().dg_workspace_size(ctypes.byref(cfg), batch, n_tokens, cache_cap)
 
 
+def _on(device):
+    """Makes `device` current where it names one: the sizes of workspaces are those of the current device."""
+    d = torch.device(device)
+    return torch.cuda.device(d) if d.type == "cuda" and d.index is not None else contextlib.nullcontext()
+
+
 def alloc_workspace(cfg: DgConfig, batch: int, n_tokens: int, cache_cap: int, device="cuda"):
-    n = dg_workspace_size(cfg, batch, n_tokens, cache_cap)
+    with _on(device):
+        n = dg_workspace_size(cfg, batch, n_tokens, cache_cap)
     if n == 0:
         raise DgError(DG_ERR_INVALID_ARG, "dg_workspace_size")
     return torch.empty(n + 256, dtype=torch.uint8, device=device)
@@ -533,7 +541,8 @@ def dg_paged_workspace_size(cfg, n_seqs, n_tokens, shared_len=0) -> int:
 
 
 def alloc_paged_workspace(cfg, n_seqs, n_tokens, shared_len=0, device="cuda"):
-    n = dg_paged_workspace_size(cfg, n_seqs, n_tokens, shared_len)
+    with _on(device):
+        n = dg_paged_workspace_size(cfg, n_seqs, n_tokens, shared_len)
     if n == 0:
         raise DgError(DG_ERR_INVALID_ARG, "dg_paged_workspace_size")
     return torch.empty(n + 256, dtype=torch.uint8, device=device)

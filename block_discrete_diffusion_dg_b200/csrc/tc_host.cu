@@ -2,6 +2,7 @@
 // point (no link-time dependency on libcuda) and the device's SM count.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdio>
 #include <mutex>
 
@@ -74,13 +75,16 @@ int make_tmap_3d_f32(CUtensorMap *out, const void *base, uint64_t d0, uint64_t d
 }
 
 int num_sms() {
-  static int n = 0;
-  if (n == 0) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (n <= 0) n = 148;
-  }
+  constexpr int DEVICES = 64, DEFAULT = 148;
+  static std::atomic<int> known[DEVICES];   // 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DEFAULT;
+  const bool keep = dev >= 0 && dev < DEVICES;
+  int n = keep ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return DEFAULT;
+  if (keep) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

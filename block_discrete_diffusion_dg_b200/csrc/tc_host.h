@@ -23,7 +23,8 @@ int make_tmap_3d(CUtensorMap *out, CUtensorMapDataType dtype, int elem_bytes, co
 int make_tmap_3d_f32(CUtensorMap *out, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
                      uint32_t b0, uint32_t b1, uint32_t b2);
 
-// Streaming multiprocessors of the current device.
+// Streaming multiprocessors of the current device (148 where it cannot be asked: sizes can be computed on a
+// host without one).  Asked once per device; safe from several threads.
 int num_sms();
 
 }  // namespace dg
