@@ -581,7 +581,6 @@ void paged_tiling(const PagedCall &c, PagedShape *p, PagedIO *io) {
   p->start_cost[PAGED_NARROW] = PAGED_TC_START_NARROW;
   p->start_cost[PAGED_FEW] = PAGED_TC_START_FEW;
   io->ctas = num_sms() * (tc ? 1 : 2);
-  p->least[PAGED_FEW] = PAGED_TC_LEAST_FEW;
   io->workers = tc ? 11 * io->ctas : io->ctas;
   const long long most = (long long)c.n_tokens * rep;
   for (int k = 0; k < 3; ++k) {

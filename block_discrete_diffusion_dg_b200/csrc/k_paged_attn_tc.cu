@@ -13,8 +13,9 @@
 //                  the start and end of one's items hide behind the other's work.
 // Few-row items (single tokens: up to 16 rows) would leave 7/8 of such a tile empty and pass each
 // key tile through a chain of four waits; there each of the eight softmax warps walks a range of
-// its own with mma.sync, 32 keys a step, from a ring of its own in the memory that the chains have
-// left, so that almost all of it is in flight: these items are bound by the bytes of their keys.
+// its own with mma.sync, 32 keys a step, from a ring of its own in the memory that chains would use (a CTA
+// serves one kind of work), so that almost all of it is in flight: these items are bound by the bytes of
+// their keys.
 // Their copies are cp.async, not TMA: a box of one 16-key page takes the TMA unit about 60 cycles
 // for 2 KB, and eight warps that each wait for several such boxes waited 3 us before their first
 // product.  Calls whose items all are few-row have a kernel of their own without the chains' code
@@ -176,11 +177,10 @@ __global__ void __launch_bounds__(P_THR, 1)
   uint64_t *q_empty = q_full + 2, *full = q_empty + 2, *empty = full + S;
   uint64_t *s_full = empty + S, *p_full = s_full + 2, *pv_done = p_full + 2, *o_empty = pv_done + 2;
   uint64_t *mma_fin = o_empty + 2;
-  uint64_t *chains_done = mma_fin + 1;
-  PagedStart *start = reinterpret_cast<PagedStart *>(chains_done + 1);   // [PAGED_STARTS]
+  PagedStart *start = reinterpret_cast<PagedStart *>(mma_fin + 1);   // [PAGED_STARTS]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + PAGED_STARTS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert((4 + 2 * S + 10) * 8 + PAGED_STARTS * sizeof(PagedStart) + 8 <= 2048, "shared memory");
+  static_assert((4 + 2 * S + 9) * 8 + PAGED_STARTS * sizeof(PagedStart) + 8 <= 2048, "shared memory");
 
   // (the shuffle tells the compiler that a warp's threads agree on it)
   const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -199,7 +199,6 @@ __global__ void __launch_bounds__(P_THR, 1)
         mbar_init(&empty[s], 1);
       }
       mbar_init(mma_fin, 1);
-      mbar_init(chains_done, 8);
       *abort_flag = 0;
       fence_mbar_init();
     }
@@ -611,16 +610,15 @@ __global__ void __launch_bounds__(P_THR, 1)
       }
     }
     // ---- few-row items
-    // this warp has left its chain; when all eight have, the rings and query tiles are idle
+    // A CTA serves one kind of work (paged_share), so a CTA that has few-row items has nothing for its
+    // chains: their query tiles and key ring are idle from the start, and hold the rings here.
     __syncwarp();
-    if (CHAINS && lane == 0) mbar_arrive(chains_done);
     const PagedStart &few_start = start[3 + warp - 4];
     if (ok && few_start.u0 < few_start.u1) {
       constexpr int ROW = HD * 2, SLOT = F_KT * ROW;            // a slot: 32 keys, chunks swizzled
       const int fw = warp - 4, gr = lane >> 2, tq = lane & 3;   // fragment row and column pair
       uint8_t *ring = sQ + fw * F_SLOTS * SLOT;
       const int shift = io.page_shift;
-      if constexpr (CHAINS) ok = __all_sync(FULL, mbar_wait(chains_done, 0));
       // Copies run F_SLOTS slots ahead of the arithmetic, across items: slot n of the walk is K (n
       // even) or V of a step, one group of cp.async each.  Rows behind the last key are filled
       // with zeros. Each lane holds the place of a page, 32 pages of a sequence at a time
@@ -639,7 +637,7 @@ __global__ void __launch_bounds__(P_THR, 1)
       int seen[2] = {0, 0};                                     // keys that rows gr and gr + 8 see
       uint32_t qf[HD / 16][4], ph[2][4], pl[2][4];
       float o[HD / 8][4], m[2], ls[2];
-      while (ok) {
+      for (;;) {
         if (lead > 0) {
           --lead;
         } else if (!v_half) {
@@ -826,7 +824,6 @@ __global__ void __launch_bounds__(P_THR, 1)
         }
         cp_commit();   // (empty at the end, so that the count of groups in flight stays the same)
       }
-      if (!ok && lane == 0) p_fail(io.status, abort_flag);
     }
   }
   if constexpr (CHAINS) {

@@ -32,7 +32,6 @@ constexpr int PAGED_TC_ROWS = 128, PAGED_TC_KT = 128;
 constexpr int PAGED_TC_FEW = 16, PAGED_TC_FEW_KT = 32;   // few-row items: rows at most, keys per step
 // Starting and storing an item, in key tiles of its kind.
 constexpr int PAGED_TC_START_WIDE = 3, PAGED_TC_START_NARROW = 1, PAGED_TC_START_FEW = 1;
-constexpr int PAGED_TC_LEAST_FEW = 1;
 inline bool paged_tc_supported(int act, int hd) { return act == DG_BF16 && (hd == 64 || hd == 128); }
 struct PagedCall;
 int launch_paged_tc(const PagedCall &c, const PagedShape &p, const PagedIO &io, cudaStream_t s);

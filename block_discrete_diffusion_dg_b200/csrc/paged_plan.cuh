@@ -39,7 +39,7 @@ struct PagedShape {
   // by kind of item:
   int kt_shift[3];          // keys per tile: 2^kt_shift
   int start_cost[3];        // cost of starting and storing an item, in key tiles
-  int least[3];             // least cost worth a worker of its own
+  int least[3];             // least cost worth a worker of its own (0 and 1: any; calls use no more)
   int causal;
   int shared_len;           // > 0: keys [0, shared_len) form segment 0, seen by every token
   int cap;                  // keys a page-table row can address
