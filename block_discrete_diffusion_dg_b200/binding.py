@@ -562,7 +562,8 @@ def dg_paged_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, q, kv: PagedKV, causal
 
 def dg_prefix_attn(cfg, n_seqs, n_tokens, seq_off, kv_len, shared_len, q, kv: PagedKV, causal, out,
                    ws, dev_status=None, stream=None):
-    """dg_paged_attn where the first shared_len keys are common to all sequences, read once."""
+    """dg_paged_attn where the first shared_len keys are common to all sequences, read once for up to
+    256 / (Hq / Hkv) packed rows: for next tokens and other sequences of few rows."""
     dev = q.get_device()
     w, wb = _scratch(ws, dev)
     heads = act, hq, _, hd = _heads(cfg)

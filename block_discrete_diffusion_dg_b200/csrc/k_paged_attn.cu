@@ -631,9 +631,10 @@ int launch_paged_attn(const PagedCall &c, void *ws, cudaStream_t s) {
   p.cap = c.max_pages * c.page_size;
   // Batches of single tokens: every item is taken for few-row, by a kernel without the chains (64
   // tokens over 64 to 16384 keys 123 -> 115 us, 16 over 500 to 1000 keys 20.4 -> 17.9).  Lengths are not
-  // known here, so the rule is a row per sequence on average; a prompt among empty sequences comes out
-  // right, but its keys are read once per 16 rows (512 rows over 4512 keys among 511 empty ones: 169 us
-  // where the chains take 46).
+  // known here, so the rule is a row per sequence on average.  A prompt among empty sequences comes out
+  // right, but its keys are read once per 16 rows: 512 rows over 4512 keys among 511 empty ones take 171 us
+  // where the chains take 45; a prompt of 40 rows beside 199 tokens over 8192 keys costs nothing (1026 us,
+  // 1044 with the chains).
   if (p.qf > 0 && (c.n_tokens <= p.qf || (c.shared_len == 0 && c.n_tokens <= c.n_seqs))) {
     PagedShape few = p;
     few.qt = few.qn = few.qf;

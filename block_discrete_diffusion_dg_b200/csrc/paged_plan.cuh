@@ -229,7 +229,8 @@ DG_HD PagedHead paged_head(const PagedShape &p, int kind, const PagedStart &st) 
 // Shares the CTAs out among the kinds that have any cost: kind k gets CTAs [first[k], first[k] +
 // count[k]).  Where each CTA took its part of every kind one after the other it paid for a start per
 // kind (first loads, code not yet fetched), and the bytes of single tokens did not overlap the matrix
-// products of wide items: 128 single tokens over a shared prefix of 8192 keys took 61 us, now 49.
+// products of wide items: 128 single tokens over a shared prefix of 8192 keys took 61 us, 49 as they are
+// shared out now (41 since the joins got shorter).
 // weight: cycles of a CTA per unit of cost on calls of one kind (wide: a key tile of both chains;
 // narrow: half of a tile of each chain; few-row: an eighth of 32 keys of each of eight warps, between
 // 300, right for many keys per token, and 500, right for a long prefix).

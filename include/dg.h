@@ -401,9 +401,9 @@ int dg_generate(const dg_config *cfg, const dg_model *model, int batch, int32_t 
  *   page ids outside [0, n_pages), record DG_ERR_INVALID_ARG; a sequence whose keys would pass
  *   max_pages * page_size records DG_ERR_CAPACITY.  Such a sequence is skipped (its output rows and
  *   pages are left as they were); where offsets descend, the attention calls leave every row as it
- *   was, and the append serves a row for one of the sequences that claim it.  But a bad page id among an attention's keys leaves that
- *   sequence's output rows (with a shared prefix, if the page is one of the prefix: every row)
- *   without meaning.  Nothing is read or written out of range.
+ *   was, and the append serves a row for one of the sequences that claim it.  But a bad page id among an
+ *   attention's keys leaves that sequence's output rows (with a shared prefix, if the page is one of the
+ *   prefix: every row) without meaning.  Nothing is read or written out of range.
  * A workspace serves one call at a time: calls that may run at once take one each. */
 
 /* One layer's pages (HOST struct).  Key j of sequence s is row j % page_size of page
@@ -470,10 +470,12 @@ size_t dg_paged_workspace_size(const dg_config *cfg, int n_seqs, int n_tokens, i
  *   [0, kv_len[s] + i] (causal = 1: a prompt, a chunk of one, or a single next token).
  *   q, out [n_tokens][Hq][hd].  out may not overlap q.
  * Scores, softmax statistics and sums are fp32; with bf16 activations of head_dim 64 or 128 the
- * softmax's numerators are rounded to bf16 for the tensor cores.  DG_ERR_UNSUPPORTED where Hq / Hkv >
- * 64, or where the sizes given (n_seqs, n_tokens, max_pages) allow more than 2^30 steps of work; a
- * step is one kv head's, up to 16 rows against 32 keys or 256 rows against 128 keys (4096 single
- * tokens, each with room for 131072 keys of 8 kv heads: 2^27).
+ * softmax's numerators are rounded to bf16 for the tensor cores, except where a sequence's tokens (or the
+ * last ones of a longer run) have at most 16 query rows per kv head: a token may come out differently, by
+ * about that rounding, alone and within a prompt.  DG_ERR_UNSUPPORTED where Hq / Hkv > 64, or where the
+ * sizes given (n_seqs, n_tokens, max_pages) allow more than 2^30 steps of work; a step is one kv head's, up
+ * to 16 rows against 32 keys or 256 rows against 128 keys (4096 single tokens, each with room for 131072
+ * keys of 8 kv heads: 2^27).
  * The values of keys a sequence holds must be finite, those of later tokens of its batch included: a
  * non-finite value may reach the rows before it. */
 int dg_paged_attn(const dg_config *cfg, int n_seqs, int n_tokens, const int32_t *seq_off,
@@ -481,8 +483,12 @@ int dg_paged_attn(const dg_config *cfg, int n_seqs, int n_tokens, const int32_t 
                   void *out, void *ws, size_t ws_bytes, int32_t *dev_status, void *stream);
 
 /* dg_paged_attn for sequences that share their first shared_len keys (continuations or canvases of
- * one long prompt): the keys of the prefix are read once for all rows instead of once for each
- * sequence, and joined with each sequence's own.  shared_len: a multiple of page_size, > 0; the
+ * one long prompt): the packed rows visit the prefix's keys together, each key once for up to
+ * 256 / (Hq / Hkv) consecutive rows (64 / (Hq / Hkv) with fp32 or head_dim 32) instead of once for each
+ * sequence, and their results are joined with those over each sequence's own keys.  It saves key traffic
+ * where sequences have few rows each (next tokens).  Sequences that fill such groups by themselves
+ * (canvases of 256 tokens) read the prefix as often in dg_paged_attn, which has no partial results to
+ * join and is the faster call for them.  shared_len: a multiple of page_size, > 0; the
  * first shared_len / page_size entries of every page-table row name the same pages (those of row 0
  * are read), and kv_len[s] >= shared_len for every sequence that has rows (DG_ERR_INVALID_ARG on
  * the device otherwise).  Other arguments and results as dg_paged_attn. */
